@@ -29,7 +29,8 @@ EXPORTS = ("attn_status_string", "attn_version", "attn_fwd", "attn_fwd_varlen", 
            "attn_fwd_window", "attn_bwd_window", "attn_bwd_deterministic_workspace_size",
            "attn_bwd_deterministic", "attn_quantize_fp8_rope", "attn_decode_fp8_workspace_size",
            "attn_decode_fp8", "attn_fwd_fp8_kv_tile", "attn_quantize_fp8_varlen", "attn_fwd_fp8_varlen",
-           "attn_fwd_fp8_window")
+           "attn_fwd_fp8_window", "attn_rope", "attn_rope_tables", "attn_cache_append_fp8",
+           "attn_decode_cache_fp8_splits", "attn_decode_cache_fp8_workspace_size", "attn_decode_cache_fp8")
 
 
 class AttnError(RuntimeError):
@@ -39,6 +40,7 @@ class AttnError(RuntimeError):
 
 
 _P, _I, _F, _Z = C.c_void_p, C.c_int, C.c_float, C.c_size_t
+_S = C.POINTER(C.c_longlong)   # three element strides (batch, head, row) in host memory
 _SIGS = {
     "attn_status_string": ([_I], C.c_char_p),
     "attn_version": ([], C.c_char_p),
@@ -64,6 +66,12 @@ _SIGS = {
     "attn_bwd_deterministic": ([_P] * 9 + [_P, _Z, _I, _I, _I, _I, _I, _F, _I, _I, _I, _P], _I),
     "attn_quantize_fp8_varlen": ([_P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P], _I),
     "attn_fwd_fp8_varlen": ([_P] * 9 + [_I, _I, _I, _I, _I, _I, _F, _I, _P], _I),
+    "attn_rope": ([_P] * 5 + [_S, _S] + [_I] * 9 + [_P], _I),
+    "attn_rope_tables": ([_P, _P, _P, C.c_longlong, _I, _I, _F, _P], _I),
+    "attn_cache_append_fp8": ([_P, _P, _S, _S] + [_P] * 9 + [_I] * 10 + [_P], _I),
+    "attn_decode_cache_fp8_splits": ([_I, _I, _I, _I], _I),
+    "attn_decode_cache_fp8_workspace_size": ([_I, _I, _I, _I], _Z),
+    "attn_decode_cache_fp8": ([_P] * 11 + [_Z] + [_I] * 6 + [_F, _F, _I, _I, _I, _P], _I),
 }
 
 
@@ -306,6 +314,129 @@ def attn_decode_fp8(q8, sq, k8, v8, sk, sv, o, lse, workspace, num_splits, seqle
                                   _ptr(lse, "lse", B * Hq, f32), _ptr(workspace, "workspace"),
                                   workspace.numel() * workspace.element_size(),
                                   B, Hq, Hkv, Nmax, d, scale, int(num_splits), _stream(stream)), "attn_decode_fp8")
+
+
+def _one_device(*tensors):
+    """Every tensor on the current device: the stream and the library's launches are there."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.device.type == "cuda" and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensor on {t.device}, but cuda:{torch.cuda.current_device()} is the current device")
+
+
+def _strided(t, name, dtype=None, shape=None):
+    """Pointer and strides of a [B, H, N, d] tensor whose rows are dense (any batch, head and row strides)."""
+    _dims(t, name, 4)
+    if t.device.type != _DEVICE_TYPE:
+        raise ValueError(f"{name} must be a {_DEVICE_TYPE} tensor, not on {t.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name} must have adjacent elements in each row (stride 1 in its last dimension)")
+    # the stride of a dimension of size 1 is never used and may be anything
+    strides = (C.c_longlong * 3)(*(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)))
+    return C.c_void_p(t.data_ptr()), strides
+
+
+def _rope_dims(rope_cos, rope_sin):
+    """Tables [n_pos, rot_dim / 2]: their pointers, rot_dim and n_pos."""
+    n_pos, half = _dims(rope_cos, "rope_cos", 2)
+    return (_ptr(rope_cos, "rope_cos", dtype=torch.float32),
+            _ptr(rope_sin, "rope_sin", dtype=torch.float32, shape=(n_pos, half)), 2 * half, n_pos)
+
+
+def attn_rope(x, y, rope_cos, rope_sin, positions=None, interleaved=False, inverse=False, stream=None):
+    """Rotary positions of x [B,H,N,d] into y (same shape and type; y may be x), any batch, head and
+    row strides: the first 2 * rope_cos.shape[1] elements of each row are turned, the rest copied.
+    Tables float32 [n_pos, rot_dim/2]; positions int32 [B,N] or None (row n at position n; a negative
+    one leaves its row of y as it was). inverse turns back: the backward pass of the rotation."""
+    B, H, N, d = _dims(x, "x", 4)
+    _one_device(x, y, rope_cos, rope_sin, positions)
+    px, sx = _strided(x, "x")
+    py, sy = _strided(y, "y", x.dtype, x.shape)
+    pc, ps, rot, n_pos = _rope_dims(rope_cos, rope_sin)
+    _check(load().attn_rope(px, py, pc, ps, _ptr(positions, "positions", dtype=torch.int32, shape=(B, N)), sx, sy,
+                            B, H, N, d, rot, n_pos, int(bool(interleaved)), int(bool(inverse)), _dtype(x),
+                            _stream(stream)), "attn_rope")
+
+
+def attn_rope_tables(rope_cos, rope_sin, inv_freq, first_position=0, amplitude=1.0, stream=None):
+    """Cosine and sine tables [n_pos, rot_dim/2] float32 of positions first_position, + 1, ...;
+    inv_freq float64 [rot_dim/2] on the device (see rope.inv_freq for the usual scalings)."""
+    _one_device(rope_cos, rope_sin, inv_freq)
+    pc, ps, rot, n_pos = _rope_dims(rope_cos, rope_sin)
+    _check(load().attn_rope_tables(pc, ps, _ptr(inv_freq, "inv_freq", rot // 2, torch.float64), int(first_position),
+                                   n_pos, rot, float(amplitude), _stream(stream)), "attn_rope_tables")
+
+
+def _cache_ptrs(k8, v8, sk, sv, block_table, B, Hkv, d):
+    """Checked pointers of a cache (k8, v8, sk, sv, block_table), its rows per sequence and its pages:
+    dense k8 [B,Hkv,Nmax,d], or pages [P,Hkv,128,d] with block_table [B,blocks]."""
+    shape = _dims(k8, "k8", 4)
+    if block_table is None:
+        rows, pages, want = shape[2], 0, (B, Hkv, shape[2], d)
+        factors = (B, Hkv, _nb(rows))
+    else:
+        tb, blocks = _dims(block_table, "block_table", 2)
+        if tb != B:
+            raise ValueError(f"block_table must have {B} rows, got {tb}")
+        rows, pages, want = 128 * blocks, shape[0], (shape[0], Hkv, 128, d)
+        factors = (pages, Hkv)
+    u8, f32 = torch.uint8, torch.float32
+    return (_ptr(k8, "k8", dtype=u8, shape=want), _ptr(v8, "v8", dtype=u8, shape=want),
+            _ptr(sk, "sk", dtype=f32, shape=factors), _ptr(sv, "sv", dtype=f32, shape=factors),
+            _ptr(block_table, "block_table", dtype=torch.int32)), rows, pages
+
+
+def attn_cache_append_fp8(k, v, k8, v8, sk, sv, seqlens, new_lens=None, block_table=None, rope_cos=None,
+                          rope_sin=None, interleaved=False, stream=None):
+    """Quantise new rows k, v [B,Hkv,n,d] (any batch, head and row strides) into a cache behind
+    seqlens[b] rows: dense k8/v8 [B,Hkv,Nmax,d], sk/sv [B,Hkv,ceil(Nmax/128)], or pages
+    [P,Hkv,128,d], [P,Hkv] with block_table int32 [B,blocks]. new_lens int32 [B]: rows of k and v that count
+    (None: all). Tables given: the keys are rotated first, row r of a sequence at position r."""
+    B, Hkv, n, d = _dims(k, "k", 4)
+    _one_device(k, v, k8, v8, sk, sv, seqlens, new_lens, block_table, rope_cos, rope_sin)
+    pk, stk = _strided(k, "k")
+    pv, stv = _strided(v, "v", k.dtype, k.shape)
+    (p8k, p8v, psk, psv, pt), rows, pages = _cache_ptrs(k8, v8, sk, sv, block_table, B, Hkv, d)
+    if (rope_cos is None) != (rope_sin is None):
+        raise ValueError("rope_cos and rope_sin go together")
+    pc, ps, rot, n_pos = _rope_dims(rope_cos, rope_sin) if rope_cos is not None else (None, None, 0, 0)
+    _check(load().attn_cache_append_fp8(pk, pv, stk, stv, p8k, p8v, psk, psv,
+                                        _ptr(seqlens, "seqlens", B, torch.int32),
+                                        _ptr(new_lens, "new_lens", B, torch.int32), pt, pc, ps, B, Hkv, n, rows,
+                                        pages, d, rot, n_pos, int(bool(interleaved)), _dtype(k), _stream(stream)),
+           "attn_cache_append_fp8")
+
+
+def attn_decode_cache_fp8_splits(B, Hq, Hkv, blocks):
+    """A number of splits that suits attn_decode_cache_fp8 (blocks: 128-row blocks per sequence)."""
+    return load().attn_decode_cache_fp8_splits(B, Hq, Hkv, blocks)
+
+
+def attn_decode_cache_fp8_workspace_size(B, Hq, d, num_splits):
+    return load().attn_decode_cache_fp8_workspace_size(B, Hq, d, num_splits)
+
+
+def attn_decode_cache_fp8(q, k8, v8, sk, sv, seqlens, o, lse, workspace, num_splits, block_table=None, slopes=None,
+                          score_cap=0.0, window_left=-1, scale=None, stream=None):
+    """One token per sequence over a block-quantised cache (dense or paged, as attn_cache_append_fp8):
+    q, o [B,Hq,d] bf16/fp16, lse [B,Hq] fp32, seqlens int32 [B] (the query stands at seqlens - 1);
+    slopes fp32 [Hq], score_cap and window_left as attn_fwd_score."""
+    B, Hq, d = _dims(q, "q", 3)
+    Hkv = _dims(k8, "k8", 4)[1]
+    _one_device(q, k8, v8, sk, sv, seqlens, o, lse, workspace, block_table, slopes)
+    (p8k, p8v, psk, psv, pt), rows, pages = _cache_ptrs(k8, v8, sk, sv, block_table, B, Hkv, d)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    _check(load().attn_decode_cache_fp8(_ptr(q, "q"), p8k, p8v, psk, psv, pt,
+                                        _ptr(seqlens, "seqlens", B, torch.int32),
+                                        _ptr(slopes, "slopes", Hq, torch.float32),
+                                        _ptr(o, "o", dtype=q.dtype, shape=(B, Hq, d)),
+                                        _ptr(lse, "lse", B * Hq, torch.float32), _ptr(workspace, "workspace"),
+                                        workspace.numel() * workspace.element_size(), B, Hq, Hkv, rows, pages, d,
+                                        scale, float(score_cap), int(window_left), int(num_splits), _dtype(q),
+                                        _stream(stream)), "attn_decode_cache_fp8")
 
 
 def attn_bwd_workspace_size(B, Hq, Hkv, N, d):

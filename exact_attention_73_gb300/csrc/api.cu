@@ -444,7 +444,7 @@ attn_status attn_get_device_status(void* stream) {
     const int zero = 0;
     if (cudaMemcpyAsync(status, &zero, sizeof(int), cudaMemcpyHostToDevice, st) != cudaSuccess) return ATTN_ERR_CUDA;
     if (cudaStreamSynchronize(st) != cudaSuccess) return ATTN_ERR_CUDA;
-    return host == kDevTimeout ? ATTN_ERR_TIMEOUT : ATTN_ERR_CUDA;
+    return host == kDevTimeout ? ATTN_ERR_TIMEOUT : host == kDevBadIndex ? ATTN_ERR_SHAPE : ATTN_ERR_CUDA;
   }
   return ATTN_OK;
 }

@@ -1,0 +1,578 @@
+// Attention of one new token per sequence over a block-quantised KV cache with
+// a 16-bit query: dense or paged cache, capped scores, distance bias, window.
+//
+//   x_j = cap tanh(scale q.k_j / cap) - slope (L - 1 - j),  O = softmax(x) V
+//
+// HBM-bound: one byte per element of K and V, read once. A product of one
+// token has at most Hq / Hkv query rows per KV head, so the tensor work is
+// small and thin: the keys (and head dims) go to the 16-row side of
+// mma.m16n8k16 and up to eight query heads to its 8-column side,
+//   S^T [16 keys x 8 heads] = K Q^T,   O^T [16 dims x 8 heads] += V^T P^T,
+// which wastes nothing at eight heads per KV head. K and V go from global
+// memory straight to registers: the contraction order of S and the dim order
+// of O are free, so each lane takes 16 consecutive bytes of a row (head dims
+// 64c + 16t .. of K, 16g .. of V) and these are its fragments as they stand,
+// after E4M3 -> FP16 (exact) and, for V, a byte interleave of two rows. P is
+// transposed by movmatrix. Nothing is staged in shared memory and no barrier
+// is waited on in the loop; the loads of the next 16 keys are issued as soon
+// as the current ones are converted.
+//
+// P~ = exp2(x - m) 2^7 in FP16 with a running max m that moves only when a
+// score passes it by 8 (log2 units), so P~ <= 2^15 and what lies 2^-31 below
+// the largest is still kept. O is held in FP32 in units of the current
+// block's V factor; both rescales are rare. Q is scaled per head to fill FP16
+// (a power of two: BF16's 8 and FP16's 11 bits stay exact).
+//
+// A CTA is one (split, 8 or 16 heads of a KV head, sequence); its four warps
+// take every fourth 16-key tile of the split and meet once, at the end. A
+// second kernel combines the splits by their log-sum-exp weights.
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/libattn.h"
+#include "lowp.cuh"
+#include "ops.h"
+#include "ptx.cuh"
+
+namespace attn {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTau = 8.f;      // the running max is left behind by up to this (log2 units)
+constexpr float kPShift = 7.f;   // P~ = 2^7 exp2(x - m) <= 2^15
+
+struct CacheDecArgs {
+  const void* q;             // [B, Hq, d]
+  const uint8_t* k8;
+  const uint8_t* v8;
+  const float* sk;
+  const float* sv;
+  const int* table;          // [B, blocks] pages, or null: dense [B, Hkv, rows_max, d]
+  const int* seqlens;        // [B]
+  const float* slopes;       // [Hq] or null
+  void* o;                   // [B, Hq, d]
+  float* lse;                // [B, Hq]
+  float* o_part;             // [splits][B * Hq][d]
+  float* lse_part;           // [splits][B * Hq]
+  int B, Hq, Hkv, group, rows_max, blocks, pages, splits, blocks_per_split, row_groups;
+  float scale_log2;          // scale * log2(e)
+  float cap, cap_log2, inv_cap;   // cap (0: none), cap * log2(e), 2 log2(e) * scale / cap
+  int window;                // keys before L - 1 - window are hidden (-1: none)
+  int* status;
+};
+
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(pair)));
+  return r;
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int N>
+__device__ __forceinline__ void load_bytes(uint32_t (&w)[N / 4], const uint8_t* p) {   // N = 8 or 16
+  if constexpr (N == 16) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = v.x; w[1] = v.y;
+  }
+}
+// x * 2^e for any e that can occur (the factor need not be a float)
+__device__ __forceinline__ float scale_pow2(float x, int e) { return ldexpf(x, e); }
+
+template <typename T, int D, int NR>
+__global__ void __launch_bounds__(32 * kWarps, (D == 256 ? 2 : NR == 2 ? 3 : 4))
+decode_cache_kernel(const CacheDecArgs a) {
+  constexpr int NG = D / 64;                     // 64-dim groups of the K contraction
+  constexpr int VB = D == 64 ? 8 : 16;           // bytes of a V row per lane and half
+  constexpr int NH = D == 256 ? 2 : 1;           // halves of a V row
+  constexpr int MT = D / 16;                     // 16-dim tiles of O^T
+  extern __shared__ float smem[];                // [kWarps][8 NR][D] partial O, then m and l
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  int item = blockIdx.x;
+  const int split = item % a.splits;
+  item /= a.splits;
+  const int rg = item % a.row_groups;
+  item /= a.row_groups;
+  const int h = item % a.Hkv, b = item / a.Hkv;
+  const int head0 = rg * 8 * NR;                 // first head of the KV head's group in this CTA
+  const int heads = min(a.group - head0, 8 * NR);
+  const long long qrow0 = static_cast<long long>(b) * a.Hq + static_cast<long long>(h) * a.group + head0;
+  // visible keys [lo, L) and this split's blocks of them
+  const int L = max(0, min(a.seqlens[b], a.rows_max));
+  const int lo = a.window >= 0 ? max(0, L - 1 - a.window) : 0;
+  const int blk0 = (lo >> 7) + split * a.blocks_per_split;
+  const int blk1 = min((L + 127) >> 7, blk0 + a.blocks_per_split);
+  if (blk0 >= blk1) {   // nothing to see in this split
+    if (a.splits > 1) {
+      if (threadIdx.x < heads) a.lse_part[static_cast<long long>(split) * a.B * a.Hq + qrow0 + threadIdx.x] = -INFINITY;
+    } else {
+      for (int i = threadIdx.x; i < heads * D; i += 32 * kWarps) static_cast<T*>(a.o)[qrow0 * D + i] = T(0.f);
+      if (threadIdx.x < heads) a.lse[qrow0 + threadIdx.x] = -INFINITY;
+    }
+    return;
+  }
+
+  // block facts, held by the lanes: lane i has block set0 + i
+  int set0 = blk0, page_l = 0;
+  float sk_l = 1.f, sv_l = 1.f;
+  auto load_set = [&](int s0) {
+    set0 = s0;
+    const int blk = s0 + lane;
+    page_l = -1;
+    if (blk < blk1) {
+      long long si;
+      if (a.table) {
+        page_l = __ldg(a.table + static_cast<long long>(b) * a.blocks + blk);
+        if (page_l < 0 || page_l >= a.pages) {   // no such page: its keys are not seen
+          page_l = -1;
+          atomicExch(a.status, kDevBadIndex);
+        }
+        si = static_cast<long long>(page_l) * a.Hkv + h;
+      } else {
+        page_l = blk;
+        si = (static_cast<long long>(b) * a.Hkv + h) * a.blocks + blk;
+      }
+      if (page_l >= 0) {
+        sk_l = __ldg(a.sk + si);
+        sv_l = __ldg(a.sv + si);
+      }
+    }
+  };
+  load_set(blk0);
+
+  // K and V of the 16 keys of tile `tile` (128-key block tile / 8): rows past
+  // the visible keys stay zero, whatever the cache holds there
+  uint32_t kr[2][NG][4];          // keys g, g + 8
+  uint32_t vr[4][NH][VB / 4];     // keys 2t, 2t + 1, 2t + 8, 2t + 9
+  auto block_base = [&](int tile) -> long long {   // byte offset of the tile's first row, -1: not there
+    const int blk = tile >> 3;
+    if (blk >= set0 + 32) load_set(blk);
+    const int page = __shfl_sync(0xffffffffu, page_l, blk - set0);
+    if (page < 0) return -1;
+    const long long row = a.table ? (static_cast<long long>(page) * a.Hkv + h) * 128
+                                  : (static_cast<long long>(b) * a.Hkv + h) * a.rows_max + static_cast<long long>(blk) * 128;
+    return (row + (tile & 7) * 16) * D;
+  };
+  auto load_k = [&](int tile, long long base) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = g + 8 * r, key = tile * 16 + row;
+      const bool in = base >= 0 && key >= lo && key < L;
+#pragma unroll
+      for (int c = 0; c < NG; ++c) {
+        if (in) {
+          load_bytes<16>(kr[r][c], a.k8 + base + row * D + 64 * c + 16 * t);
+        } else {
+          kr[r][c][0] = kr[r][c][1] = kr[r][c][2] = kr[r][c][3] = 0;
+        }
+      }
+    }
+  };
+  auto load_v = [&](int tile, long long base) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 2 * t + (r & 1) + 8 * (r >> 1), key = tile * 16 + row;
+      const bool in = base >= 0 && key >= lo && key < L;
+#pragma unroll
+      for (int c = 0; c < NH; ++c) {
+        if (in) {
+          load_bytes<VB>(vr[r][c], a.v8 + base + row * D + 128 * c + VB * g);
+        } else {
+#pragma unroll
+          for (int i = 0; i < VB / 4; ++i) vr[r][c][i] = 0;
+        }
+      }
+    }
+  };
+  const int tile_end = min(blk1 * 8, (L + 15) >> 4);
+  int tile = max(blk0 * 8, lo >> 4) + warp;
+  long long base = -1;
+  if (tile < tile_end) {
+    base = block_base(tile);
+    load_k(tile, base);
+    load_v(tile, base);
+  }
+
+  // Q^T fragments: head g (of each eight), the dims of this lane's K bytes
+  uint32_t qf[NR][NG][4][2];
+  float qscale[NR][2];            // scale * log2(e) (or 2 log2(e) scale / cap) / 2^e of heads 2t, 2t + 1
+  float slope2[NR][2];            // slope * log2(e) of the same heads
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    const bool in = 8 * n + g < heads;
+    const T* q = static_cast<const T*>(a.q) + (qrow0 + 8 * n + g) * D;
+    uint4 w[NG][2];
+    float amax = 0.f;
+#pragma unroll
+    for (int c = 0; c < NG; ++c)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        w[c][u] = in ? __ldg(reinterpret_cast<const uint4*>(q + 64 * c + 16 * t) + u) : make_uint4(0, 0, 0, 0);
+        float f[8];
+        unpack8<T>(w[c][u], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
+      }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    int ex = 0;
+    if (amax > 0.f) frexpf(amax, &ex);
+    ex = 15 - ex;                 // amax 2^ex in [2^14, 2^15)
+#pragma unroll
+    for (int c = 0; c < NG; ++c)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float f[8];
+        unpack8<T>(w[c][u], f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          qf[n][c][2 * u + (i >> 1)][i & 1] = pack_f16x2(scale_pow2(f[2 * i], ex), scale_pow2(f[2 * i + 1], ex));
+      }
+    const float mul = a.cap > 0.f ? a.inv_cap : a.scale_log2;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int col = 2 * t + u;  // this lane's columns of S^T and O^T
+      qscale[n][u] = scale_pow2(mul, -__shfl_sync(0xffffffffu, ex, 4 * col));
+      slope2[n][u] = a.slopes && 8 * n + col < heads
+                         ? __ldg(a.slopes + static_cast<long long>(h) * a.group + head0 + 8 * n + col) * kLog2e : 0.f;
+    }
+  }
+
+  float acc[NR][MT][4];
+  float m[NR][2], l[NR][2];
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[n][i][e] = 0.f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      m[n][u] = -INFINITY;
+      l[n][u] = 0.f;
+    }
+  }
+  int f_cur = 0;                  // O is held in units of 2^f_cur
+  bool first = true;
+
+  for (; tile < tile_end; tile += kWarps) {
+    const int blk = tile >> 3;
+    const float sk = __shfl_sync(0xffffffffu, sk_l, blk - set0), sv = __shfl_sync(0xffffffffu, sv_l, blk - set0);
+    float s[NR][4];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+    for (int c = 0; c < NG; ++c)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t a0 = e4m3x2_to_f16x2(kr[0][c][w]), a2 = e4m3x2_to_f16x2(kr[0][c][w] >> 16);
+        const uint32_t a1 = e4m3x2_to_f16x2(kr[1][c][w]), a3 = e4m3x2_to_f16x2(kr[1][c][w] >> 16);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) mma_16816(s[n], a0, a1, a2, a3, qf[n][c][w][0], qf[n][c][w][1]);
+      }
+    const bool here = base >= 0;
+    const int next = tile + kWarps;
+    const bool more = next < tile_end;
+    long long base_next = -1;
+    if (more) {
+      base_next = block_base(next);
+      load_k(next, base_next);
+    }
+    // scores in log2 units: values 0, 1 are key g, values 2, 3 key g + 8, of heads 2t and 2t + 1
+    const int key0 = tile * 16 + g;
+    const bool edge = !here || tile * 16 < lo || tile * 16 + 16 > L;
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x = s[n][e] * (qscale[n][e & 1] * sk);
+        if (a.cap > 0.f) x = a.cap_log2 - 2.f * a.cap_log2 * rcp_approx(1.f + ex2(x));   // cap tanh(z), x = 2 z log2(e)
+        const int key = key0 + 8 * (e >> 1);
+        if (a.slopes) x -= slope2[n][e & 1] * static_cast<float>(L - 1 - key);
+        if (edge && (!here || key < lo || key >= L)) x = -INFINITY;
+        s[n][e] = x;
+      }
+    // move the running max where a score passes it by more than kTau
+    bool up = false;
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) up |= fmaxf(s[n][u], s[n][2 + u]) > m[n][u] + kTau;
+    if (warp_any(up)) {
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float mx = fmaxf(s[n][u], s[n][2 + u]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          if (mx > m[n][u]) {
+            const float corr = ex2(m[n][u] - mx);   // 0 from -inf
+            m[n][u] = mx;
+            l[n][u] *= corr;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              acc[n][i][u] *= corr;
+              acc[n][i][2 + u] *= corr;
+            }
+          }
+        }
+    }
+    const int f_j = static_cast<int>((__float_as_uint(sv) >> 23) & 0xffu) - 127;
+    if (here && (first || f_j != f_cur)) {   // a block with another V factor: O to its units
+      if (!first) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][i][e] = scale_pow2(acc[n][i][e], f_cur - f_j);
+      }
+      f_cur = f_j;
+      first = false;
+    }
+    uint32_t pb[NR][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const float mu0 = (m[n][0] == -INFINITY ? 0.f : m[n][0]) - kPShift;
+      const float mu1 = (m[n][1] == -INFINITY ? 0.f : m[n][1]) - kPShift;
+      const float p0 = ex2(s[n][0] - mu0), p1 = ex2(s[n][1] - mu1), p2 = ex2(s[n][2] - mu0), p3 = ex2(s[n][3] - mu1);
+      l[n][0] += p0 + p2;
+      l[n][1] += p1 + p3;
+      pb[n][0] = transpose_8x8(pack_f16x2(p0, p1));
+      pb[n][1] = transpose_8x8(pack_f16x2(p2, p3));
+    }
+#pragma unroll
+    for (int c = 0; c < NH; ++c)
+#pragma unroll
+      for (int w = 0; w < VB / 4; ++w) {
+        const uint32_t k01a = __byte_perm(vr[0][c][w], vr[1][c][w], 0x5140), k01b = __byte_perm(vr[0][c][w], vr[1][c][w], 0x7362);
+        const uint32_t k89a = __byte_perm(vr[2][c][w], vr[3][c][w], 0x5140), k89b = __byte_perm(vr[2][c][w], vr[3][c][w], 0x7362);
+        const int i = c * (VB / 2) + 2 * w;
+        const uint32_t a0 = e4m3x2_to_f16x2(k01a), a1 = e4m3x2_to_f16x2(k01a >> 16);
+        const uint32_t a2 = e4m3x2_to_f16x2(k89a), a3 = e4m3x2_to_f16x2(k89a >> 16);
+        const uint32_t b0 = e4m3x2_to_f16x2(k01b), b1 = e4m3x2_to_f16x2(k01b >> 16);
+        const uint32_t b2 = e4m3x2_to_f16x2(k89b), b3 = e4m3x2_to_f16x2(k89b >> 16);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          mma_16816(acc[n][i], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+          mma_16816(acc[n][i + 1], b0, b1, b2, b3, pb[n][0], pb[n][1]);
+        }
+      }
+    if (more) load_v(next, base_next);
+    base = base_next;
+  }
+
+  // join the warps: the largest m, then sums of O and l at it
+  float* sm = smem + kWarps * 8 * NR * D;    // [kWarps][8 NR] m, then l
+  float* sl = sm + kWarps * 8 * NR;
+#pragma unroll
+  for (int n = 0; n < NR; ++n)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[n][u] += __shfl_xor_sync(0xffffffffu, l[n][u], o);
+      if (g == 0) {
+        sm[warp * 8 * NR + 8 * n + 2 * t + u] = m[n][u];
+        sl[warp * 8 * NR + 8 * n + 2 * t + u] = l[n][u];
+      }
+    }
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < NR; ++n)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int col = 8 * n + 2 * t + u;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm[w * 8 * NR + col]);
+      const float corr = m[n][u] == -INFINITY ? 0.f : ex2(m[n][u] - mx);
+      float* dst = smem + (warp * 8 * NR + col) * D;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        // tile i holds head dims (chunk base of lane group g) + 2 (i mod tiles per half), + 1
+        const int dim = (i / (VB / 2)) * 128 + VB * g + 2 * (i % (VB / 2));
+        *reinterpret_cast<float2*>(dst + dim) = make_float2(scale_pow2(acc[n][i][u] * corr, f_cur),
+                                                            scale_pow2(acc[n][i][2 + u] * corr, f_cur));
+      }
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < heads * (D / 2); i += 32 * kWarps) {
+    const int col = i / (D / 2), dim = 2 * (i % (D / 2));
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm[w * 8 * NR + col]);
+    float tot = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float mw = sm[w * 8 * NR + col];
+      tot += mw == -INFINITY ? 0.f : sl[w * 8 * NR + col] * ex2(mw - mx);
+      const float2 v = *reinterpret_cast<const float2*>(smem + (w * 8 * NR + col) * D + dim);
+      x += v.x;
+      y += v.y;
+    }
+    const float inv = tot > 0.f ? 1.f / tot : 0.f;   // every block missing: O = 0
+    const float z = mx == -INFINITY ? -INFINITY : (mx + log2f(tot) - kPShift) * 0.69314718055994530942f;
+    const long long row = qrow0 + col;
+    if (a.splits > 1) {
+      const long long pr = static_cast<long long>(split) * a.B * a.Hq + row;
+      *reinterpret_cast<float2*>(a.o_part + pr * D + dim) = make_float2(x * inv, y * inv);
+      if (dim == 0) a.lse_part[pr] = z;
+    } else {
+      const uint32_t pk = std::is_same<T, __nv_bfloat16>::value ? pack_bf16x2(x * inv, y * inv) : pack_f16x2(x * inv, y * inv);
+      *reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + row * D + dim) = pk;
+      if (dim == 0) a.lse[row] = z;
+    }
+  }
+}
+
+// One CTA per (sequence, query head), one thread per two head dims.
+template <typename T>
+__global__ void __launch_bounds__(128) combine_kernel(const float* __restrict__ o_part, const float* __restrict__ lse_part,
+                                                      T* __restrict__ o, float* __restrict__ lse, int splits, int rows,
+                                                      int d) {
+  const int r = blockIdx.x, t = threadIdx.x;
+  float mx = -INFINITY;
+  for (int s = 0; s < splits; ++s) mx = fmaxf(mx, lse_part[static_cast<long long>(s) * rows + r]);
+  float tot = 0.f, x = 0.f, y = 0.f;
+  for (int s = 0; s < splits; ++s) {
+    const float z = lse_part[static_cast<long long>(s) * rows + r];
+    if (z == -INFINITY) continue;   // nothing seen: its O was not written
+    const float w = expf(z - mx);
+    const float2 v = *reinterpret_cast<const float2*>(o_part + (static_cast<long long>(s) * rows + r) * d + 2 * t);
+    tot += w;
+    x += w * v.x;
+    y += w * v.y;
+  }
+  const float inv = tot > 0.f ? 1.f / tot : 0.f;
+  const uint32_t pk = std::is_same<T, __nv_bfloat16>::value ? pack_bf16x2(x * inv, y * inv) : pack_f16x2(x * inv, y * inv);
+  *reinterpret_cast<uint32_t*>(o + static_cast<long long>(r) * d + 2 * t) = pk;
+  if (t == 0) lse[r] = mx == -INFINITY ? -INFINITY : mx + logf(tot);
+}
+
+template <typename T, int D, int NR>
+cudaError_t launch_decode(const CacheDecArgs& a, cudaStream_t st) {
+  constexpr int SMEM = (kWarps * 8 * NR * D + 2 * kWarps * 8 * NR) * 4;
+  cudaError_t e = smem_attr_once<decode_cache_kernel<T, D, NR>>(SMEM);
+  if (e != cudaSuccess) return e;
+  const long long grid = static_cast<long long>(a.B) * a.Hkv * a.row_groups * a.splits;
+  decode_cache_kernel<T, D, NR><<<static_cast<unsigned>(grid), 32 * kWarps, SMEM, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
+  combine_kernel<T><<<static_cast<unsigned>(a.B * a.Hq), D / 2, 0, st>>>(a.o_part, a.lse_part, static_cast<T*>(a.o),
+                                                                         a.lse, a.splits, a.B * a.Hq, D);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_decode_dim(int d, const CacheDecArgs& a, cudaStream_t st) {
+  const bool wide = a.group > 8;   // 16 heads per CTA: the cache is read once for both eights
+  switch (d) {
+    case 64: return wide ? launch_decode<T, 64, 2>(a, st) : launch_decode<T, 64, 1>(a, st);
+    case 128: return wide ? launch_decode<T, 128, 2>(a, st) : launch_decode<T, 128, 1>(a, st);
+    default: return wide ? launch_decode<T, 256, 2>(a, st) : launch_decode<T, 256, 1>(a, st);
+  }
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+int heads_per_cta(int group) { return group > 8 ? 16 : 8; }
+
+}  // namespace
+
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" int attn_decode_cache_fp8_splits(int B, int Hq, int Hkv, int blocks) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || blocks < 1) return 0;
+  const int group = Hq / Hkv, per = heads_per_cta(group);
+  const long long items = static_cast<long long>(B) * Hkv * ((group + per - 1) / per);
+  // enough CTAs for four waves of four per SM (ragged lengths even out), of two blocks or more
+  const long long want = (16LL * 152 + items - 1) / items;
+  const long long most = (blocks + 1) / 2;
+  return static_cast<int>(want < 1 ? 1 : want < most ? want : most);
+}
+
+extern "C" size_t attn_decode_cache_fp8_workspace_size(int B, int Hq, int d, int num_splits) {
+  return num_splits == 1 ? 256 : attn_decode_fp8_workspace_size(B, Hq, d, num_splits);
+}
+
+extern "C" attn_status attn_decode_cache_fp8(const void* q, const void* k8, const void* v8, const float* sk,
+                                             const float* sv, const int* block_table, const int* seqlens,
+                                             const float* slopes, void* o, float* lse, void* workspace,
+                                             size_t ws_bytes, int B, int Hq, int Hkv, int Nmax, int num_pages, int d,
+                                             float scale, float score_cap, int window_left, int num_splits,
+                                             attn_dtype dtype, void* stream) {
+  if (!q || !k8 || !v8 || !sk || !sv || !seqlens || !o || !lse || !workspace) return ATTN_ERR_NULL;
+  const void* ptrs[] = {q, k8, v8, sk, sv, block_table, seqlens, slopes, o, lse, workspace};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return ATTN_ERR_ALIGN;
+  if (B < 1 || B > 65535 || Hq < 1 || Hkv < 1 || Nmax < 1 || Nmax > 0x7fffff00 || window_left < -1) return ATTN_ERR_SHAPE;
+  if (block_table && (num_pages < 1 || Nmax % 128)) return ATTN_ERR_SHAPE;
+  if (!(score_cap >= 0.f) || std::isinf(score_cap)) return ATTN_ERR_SHAPE;
+  if (d != 64 && d != 128 && d != 256) return ATTN_ERR_HEADDIM;
+  if (Hq % Hkv) return ATTN_ERR_GQA;
+  if (dtype != ATTN_BF16 && dtype != ATTN_FP16) return ATTN_ERR_DTYPE;
+  const int blocks = (Nmax + 127) / 128;
+  if (num_splits < 1 || num_splits > blocks) return ATTN_ERR_SHAPE;
+  if (static_cast<long long>(B) * Hq > INT_MAX) return ATTN_ERR_SHAPE;
+  if (ws_bytes < attn_decode_cache_fp8_workspace_size(B, Hq, d, num_splits)) return ATTN_ERR_WORKSPACE;
+  CacheDecArgs a{};
+  a.group = Hq / Hkv;
+  const int per = heads_per_cta(a.group);
+  a.row_groups = (a.group + per - 1) / per;
+  a.blocks_per_split = (blocks + num_splits - 1) / num_splits;
+  a.splits = (blocks + a.blocks_per_split - 1) / a.blocks_per_split;   // those that hold a block
+  if (static_cast<long long>(B) * Hkv * a.row_groups * a.splits > INT_MAX) return ATTN_ERR_SHAPE;
+  int* status;
+  attn_status s = device_context(&status);
+  if (s != ATTN_OK) return s;
+  a.q = q;
+  a.k8 = static_cast<const uint8_t*>(k8);
+  a.v8 = static_cast<const uint8_t*>(v8);
+  a.sk = sk;
+  a.sv = sv;
+  a.table = block_table;
+  a.seqlens = seqlens;
+  a.slopes = slopes;
+  a.o = o;
+  a.lse = lse;
+  const size_t rows = static_cast<size_t>(num_splits) * B * Hq;
+  a.o_part = static_cast<float*>(workspace);
+  a.lse_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (rows * d * 4 + 255) / 256 * 256);
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.rows_max = Nmax;
+  a.blocks = blocks;
+  a.pages = num_pages;
+  a.scale_log2 = scale * kLog2e;
+  a.cap = score_cap;
+  a.cap_log2 = score_cap * kLog2e;
+  a.inv_cap = score_cap > 0.f ? 2.f * kLog2e * scale / score_cap : 0.f;
+  a.window = window_left;
+  a.status = status;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return launch_status(dtype == ATTN_BF16 ? launch_decode_dim<__nv_bfloat16>(d, a, st)
+                                          : launch_decode_dim<__half>(d, a, st));
+}

@@ -11,6 +11,12 @@ namespace attn {
 
 attn_status device_context(int** status);
 
+// Status code of a launch's CUDA error.
+inline attn_status launch_status(cudaError_t e) {
+  if (e == cudaSuccess) return ATTN_OK;
+  return e == cudaErrorInvalidValue || e == cudaErrorLaunchOutOfResources ? ATTN_ERR_LAUNCH : ATTN_ERR_CUDA;
+}
+
 // Argument checks of the dense backward (pointers, alignment, shape, head
 // dimension, GQA, dtype, workspace), all on the host before any device work.
 attn_status bwd_check_dense(const void* q, const void* k, const void* v, const void* o, const float* lse,

@@ -26,6 +26,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "lowp.cuh"
 #include "ops.h"
 #include "ptx.cuh"
 
@@ -78,20 +79,6 @@ __device__ __forceinline__ void fwht_row(float (&x)[EPL], int li) {
       }
     }
   }
-}
-
-// Largest e with amax * 2^e <= 448 (448 = 0.875 * 2^9), 0 for amax == 0.
-__device__ __forceinline__ int e4m3_scale_exponent(float amax) {
-  if (!(amax > 0.f)) return 0;
-  int k;
-  const float m = frexpf(amax, &k);   // amax = m * 2^k, m in [0.5, 1)
-  return (m <= 0.875f) ? 9 - k : 8 - k;
-}
-
-template <typename T>
-__device__ __forceinline__ float to_f32(uint32_t bits16) {
-  if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(bits16 << 16);
-  else return __half2float(__ushort_as_half(static_cast<unsigned short>(bits16)));
 }
 
 // Where a CTA's 128-row block lives. Dense [B, H, N, d]: grid (blocks, H,

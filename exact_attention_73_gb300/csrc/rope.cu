@@ -1,0 +1,258 @@
+// Rotary positions: rotation of the leading rot_dim elements of each head row
+// (either pairing, either direction, arbitrary row, head and batch strides)
+// and the cosine and sine tables it reads.
+//
+// Rotation. With c = cos, s = sin of a row's position and pair i:
+//   a' = a c - b s,  b' = b c + a s        (inverse: s -> -s, the transpose)
+// where (a, b) is (x[i], x[i + rot/2]) or, interleaved, (x[2i], x[2i + 1]).
+// HBM-bound: 2 bytes in and 2 out per element; the tables (8 bytes per pair
+// and position) are shared by the heads. A thread owns 8 pairs of one
+// position (two 16-byte vectors; past rot_dim 16 elements that are copied),
+// loads their cosines and sines once and walks kHeads heads, so a table entry
+// is fetched once per kHeads rows and the loads of four heads are in flight
+// together. The rows of a warp are consecutive positions, so its vectors
+// cover whole 128-byte lines in both layouts.
+//
+// Tables. The angle of position p and frequency f is p f modulo one turn. In
+// floating point a far position loses the low bits that decide the angle; here
+// f / (2 pi) modulo 1 is a 64-bit fixed-point number of turns and p times it
+// modulo 2^64 is exact, so the error does not grow with p beyond that of f
+// itself (p 2^-53 turns). The top bits pick the quadrant and the rest, within
+// an eighth of a turn, goes to sincospif.
+#include <climits>
+#include <cstdint>
+
+#include "../../include/libattn.h"
+#include "lowp.cuh"
+#include "ops.h"
+#include "ptx.cuh"
+
+namespace attn {
+
+namespace {
+
+struct RopeArgs {
+  const void* x;
+  void* y;
+  const float* cos;        // [n_pos, rot_dim / 2]
+  const float* sin;
+  const int* positions;    // [B, N] or null (row n at position n)
+  long long x_sb, x_sh, x_sn, y_sb, y_sh, y_sn;   // element strides: batch, head, row
+  long long rows;          // B * N
+  int H, N, rot_dim, n_pos;
+  float sign;              // -1: inverse
+  int* status;
+};
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) return pack_bf16x2(lo, hi);
+  else return pack_f16x2(lo, hi);
+}
+
+template <typename T, int D, bool kInterleaved, int kHeads>
+__global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
+  constexpr int CH = D / 16;   // 16-element chunks per row, one per thread
+  const long long r = static_cast<long long>(blockIdx.x) * (256 / CH) + threadIdx.x / CH;
+  if (r >= a.rows) return;
+  const int c = threadIdx.x % CH;
+  const long long b = r / a.N;
+  const int n = static_cast<int>(r - b * a.N);
+  const int p = a.positions ? a.positions[r] : n;
+  if (p < 0 || p >= a.n_pos) {   // a padding row (negative) or a position past the tables: left as it is
+    if (p >= 0) atomicExch(a.status, kDevBadIndex);
+    return;
+  }
+  const bool rotated = 16 * c < a.rot_dim;
+  const int half = a.rot_dim / 2;
+  // element offsets of the thread's two vectors within the row
+  const int e0 = rotated && !kInterleaved ? 8 * c : 16 * c;
+  const int e1 = rotated && !kInterleaved ? half + 8 * c : 16 * c + 8;
+  float cs[8], sn[8];
+  if (rotated) {
+    const long long t = static_cast<long long>(p) * half + 8 * c;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(a.cos + t) + q);
+      const float4 w = __ldg(reinterpret_cast<const float4*>(a.sin + t) + q);
+      cs[4 * q] = u.x; cs[4 * q + 1] = u.y; cs[4 * q + 2] = u.z; cs[4 * q + 3] = u.w;
+      sn[4 * q] = w.x * a.sign; sn[4 * q + 1] = w.y * a.sign; sn[4 * q + 2] = w.z * a.sign; sn[4 * q + 3] = w.w * a.sign;
+    }
+  }
+  const int h0 = blockIdx.y * kHeads;
+  const T* x = static_cast<const T*>(a.x) + b * a.x_sb + static_cast<long long>(n) * a.x_sn;
+  T* y = static_cast<T*>(a.y) + b * a.y_sb + static_cast<long long>(n) * a.y_sn;
+  constexpr int U = kHeads < 4 ? kHeads : 4;   // heads whose loads are in flight together
+#pragma unroll 1
+  for (int hb = 0; hb < kHeads; hb += U) {
+    uint4 w0[U], w1[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + hb + u;
+      if (h < a.H) {
+        w0[u] = *reinterpret_cast<const uint4*>(x + h * a.x_sh + e0);
+        w1[u] = *reinterpret_cast<const uint4*>(x + h * a.x_sh + e1);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + hb + u;
+      if (h >= a.H) break;
+      if (rotated) {
+        float v0[8], v1[8];
+        unpack8<T>(w0[u], v0);
+        unpack8<T>(w1[u], v1);
+        uint32_t o0[4], o1[4];
+        if constexpr (kInterleaved) {   // pairs (0, 1), (2, 3), ... of the 16 elements
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o0[i] = pack16<T>(v0[2 * i] * cs[i] - v0[2 * i + 1] * sn[i], v0[2 * i + 1] * cs[i] + v0[2 * i] * sn[i]);
+            o1[i] = pack16<T>(v1[2 * i] * cs[4 + i] - v1[2 * i + 1] * sn[4 + i],
+                              v1[2 * i + 1] * cs[4 + i] + v1[2 * i] * sn[4 + i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o0[i] = pack16<T>(v0[2 * i] * cs[2 * i] - v1[2 * i] * sn[2 * i],
+                              v0[2 * i + 1] * cs[2 * i + 1] - v1[2 * i + 1] * sn[2 * i + 1]);
+            o1[i] = pack16<T>(v1[2 * i] * cs[2 * i] + v0[2 * i] * sn[2 * i],
+                              v1[2 * i + 1] * cs[2 * i + 1] + v0[2 * i + 1] * sn[2 * i + 1]);
+          }
+        }
+        w0[u] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+        w1[u] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+      }
+      *reinterpret_cast<uint4*>(y + h * a.y_sh + e0) = w0[u];
+      *reinterpret_cast<uint4*>(y + h * a.y_sh + e1) = w1[u];
+    }
+  }
+}
+
+template <typename T, int D, bool kInterleaved>
+cudaError_t launch_rope_heads(const RopeArgs& a, cudaStream_t st) {
+  constexpr int ROWS = 256 / (D / 16);
+  const long long gx = (a.rows + ROWS - 1) / ROWS;
+  // one head per thread while that still leaves every SM few warps (single
+  // tokens: latency), else eight heads per table entry
+  const bool few = gx * ((a.H + 7) / 8) < 2 * 152;
+  const int per = few ? 1 : 8;
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>((a.H + per - 1) / per));
+  if (few) rope_kernel<T, D, kInterleaved, 1><<<grid, 256, 0, st>>>(a);
+  else rope_kernel<T, D, kInterleaved, 8><<<grid, 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_rope(int d, bool interleaved, const RopeArgs& a, cudaStream_t st) {
+  switch (d) {
+    case 64: return interleaved ? launch_rope_heads<T, 64, true>(a, st) : launch_rope_heads<T, 64, false>(a, st);
+    case 128: return interleaved ? launch_rope_heads<T, 128, true>(a, st) : launch_rope_heads<T, 128, false>(a, st);
+    default: return interleaved ? launch_rope_heads<T, 256, true>(a, st) : launch_rope_heads<T, 256, false>(a, st);
+  }
+}
+
+// One thread per four pairs, walking kTablePos positions: the fixed-point step
+// is made once, and each further position adds it.
+constexpr int kTablePos = 8;
+
+__global__ void __launch_bounds__(256) rope_tables_kernel(float* __restrict__ cos_t, float* __restrict__ sin_t,
+                                                          const double* __restrict__ inv_freq, long long first,
+                                                          int n_pos, int half, float amplitude) {
+  const int quads = half / 4;
+  const long long id = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const long long p0 = id / quads * kTablePos;
+  if (p0 >= n_pos) return;
+  const int i0 = static_cast<int>(id % quads) * 4;
+  unsigned long long step[4], at[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    double turns = inv_freq[i0 + u] * 0.15915494309189533577;   // 1 / (2 pi)
+    turns -= floor(turns);
+    // turns < 1 keeps 53 bits; 2^64 turns modulo 2^64 (a turn that rounded up to 1 is 0)
+    step[u] = turns < 1.0 ? static_cast<unsigned long long>(turns * 18446744073709551616.0) : 0ull;
+    at[u] = static_cast<unsigned long long>(first + p0) * step[u];
+  }
+  for (int k = 0; k < kTablePos && p0 + k < n_pos; ++k) {
+    float c[4], s[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t turn = static_cast<uint32_t>(at[u] >> 32);   // 2^32 per turn
+      const uint32_t quadrant = (turn + 0x20000000u) >> 30;       // nearest quarter turn
+      const int rest = static_cast<int>(turn - (quadrant << 30)); // within an eighth of a turn
+      float sr, cr;
+      sincospif(static_cast<float>(rest) * 4.656612873077393e-10f, &sr, &cr);   // rest * 2^-31 half turns
+      const float cq = quadrant & 1 ? sr : cr, sq = quadrant & 1 ? cr : sr;
+      c[u] = (((quadrant + 1) & 2) ? -cq : cq) * amplitude;
+      s[u] = ((quadrant & 2) ? -sq : sq) * amplitude;
+      at[u] += step[u];
+    }
+    const long long o = (p0 + k) * half + i0;
+    *reinterpret_cast<float4*>(cos_t + o) = make_float4(c[0], c[1], c[2], c[3]);
+    *reinterpret_cast<float4*>(sin_t + o) = make_float4(s[0], s[1], s[2], s[3]);
+  }
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" attn_status attn_rope(const void* x, void* y, const float* rope_cos, const float* rope_sin,
+                                 const int* positions, const long long* x_strides, const long long* y_strides, int B,
+                                 int H, int N, int d, int rot_dim, int n_pos, int interleaved, int inverse,
+                                 attn_dtype dtype, void* stream) {
+  if (!x || !y || !rope_cos || !rope_sin || !x_strides || !y_strides) return ATTN_ERR_NULL;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(rope_cos) || !aligned16(rope_sin) ||
+      (positions && !aligned16(positions)))
+    return ATTN_ERR_ALIGN;
+  if (B < 1 || B > 65535 || H < 1 || H > 65535 || N < 1 || n_pos < 1) return ATTN_ERR_SHAPE;
+  if (!positions && N > n_pos) return ATTN_ERR_SHAPE;
+  if (d != 64 && d != 128 && d != 256) return ATTN_ERR_HEADDIM;
+  if (rot_dim < 16 || rot_dim > d || rot_dim % 16) return ATTN_ERR_SHAPE;
+  if (dtype != ATTN_BF16 && dtype != ATTN_FP16) return ATTN_ERR_DTYPE;
+  for (int i = 0; i < 3; ++i)   // rows are read and written in 16-byte vectors
+    if (x_strides[i] % 8 || y_strides[i] % 8) return ATTN_ERR_ALIGN;
+  const long long rows = static_cast<long long>(B) * N;
+  if ((rows + 256 / (d / 16) - 1) / (256 / (d / 16)) > INT_MAX) return ATTN_ERR_SHAPE;
+  int* status;
+  attn_status s = device_context(&status);
+  if (s != ATTN_OK) return s;
+  RopeArgs a{};
+  a.x = x;
+  a.y = y;
+  a.cos = rope_cos;
+  a.sin = rope_sin;
+  a.positions = positions;
+  a.x_sb = x_strides[0]; a.x_sh = x_strides[1]; a.x_sn = x_strides[2];
+  a.y_sb = y_strides[0]; a.y_sh = y_strides[1]; a.y_sn = y_strides[2];
+  a.rows = rows;
+  a.H = H;
+  a.N = N;
+  a.rot_dim = rot_dim;
+  a.n_pos = n_pos;
+  a.sign = inverse ? -1.f : 1.f;
+  a.status = status;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return launch_status(dtype == ATTN_BF16 ? launch_rope<__nv_bfloat16>(d, interleaved != 0, a, st)
+                                          : launch_rope<__half>(d, interleaved != 0, a, st));
+}
+
+extern "C" attn_status attn_rope_tables(float* rope_cos, float* rope_sin, const double* inv_freq,
+                                        long long first_position, int n_pos, int rot_dim, float amplitude,
+                                        void* stream) {
+  if (!rope_cos || !rope_sin || !inv_freq) return ATTN_ERR_NULL;
+  if (!aligned16(rope_cos) || !aligned16(rope_sin) || !aligned16(inv_freq)) return ATTN_ERR_ALIGN;
+  if (n_pos < 1 || first_position < 0 || first_position > (1LL << 40) || rot_dim < 16 || rot_dim > 256 || rot_dim % 16)
+    return ATTN_ERR_SHAPE;
+  int* status;
+  attn_status s = device_context(&status);
+  if (s != ATTN_OK) return s;
+  const int half = rot_dim / 2;
+  const long long threads = (static_cast<long long>(n_pos) + kTablePos - 1) / kTablePos * (half / 4);
+  rope_tables_kernel<<<static_cast<unsigned>((threads + 255) / 256), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+      rope_cos, rope_sin, inv_freq, first_position, n_pos, half, amplitude);
+  return launch_status(cudaGetLastError());
+}

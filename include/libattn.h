@@ -27,7 +27,8 @@
  *   - causal: key j is visible to query i iff j <= i (positions counted
  *     inside each sequence; queries and keys have the same length).
  *   - LSE is float32, natural log: dense [B, Hq, N], packed [Hq, T].
- *   - All pointers are device pointers owned by the caller; the library
+ *   - All pointers are device pointers owned by the caller (attn_rope's and
+ *     attn_cache_append_fp8's stride arrays are host memory); the library
  *     never allocates or frees device memory and never synchronises.
  *     Every pointer must be 16-byte aligned.
  *   - stream is a cudaStream_t passed as void* (NULL = legacy default
@@ -244,6 +245,117 @@ ATTN_API attn_status attn_decode_fp8(const void* q8, const float* sq, const void
                                      void* workspace, size_t ws_bytes, int B, int Hq, int Hkv, int Nmax, int d,
                                      float scale, int num_splits, void* stream);
 
+/*
+ * Rotary positions by themselves, for 16-bit attention, for single tokens and
+ * for the backward pass (attn_quantize_fp8_rope fuses them into the
+ * quantiser). Row (b, h, n) of x
+ * [B,H,N,d], d in {64, 128, 256}, has position p = positions[b,n] (int32
+ * [B,N] on the device; NULL: p = n) and its first rot_dim elements (a
+ * multiple of 16, 16 <= rot_dim <= d) are turned in pairs i < rot_dim/2 with
+ * c = cos[p,i], s = sin[p,i] of the float32 tables [n_pos, rot_dim/2]:
+ *   a' = a c - b s,  b' = b c + a s
+ * with (a, b) = (x[i], x[i + rot_dim/2]), or (x[2i], x[2i+1]) if interleaved;
+ * the other elements are copied. Computed in float32, rounded once.
+ * inverse != 0 turns back (s -> -s): that is the transpose, so it is the
+ * backward pass of the rotation for the gradient of y.
+ * x_strides, y_strides: HOST arrays of three element strides (batch, head,
+ * row), multiples of 8; elements of a row are adjacent. y may be x itself
+ * with the same strides; any other overlap is not allowed. A row whose
+ * position is negative is padding: its row of y is left as it was. So is a
+ * row whose position is n_pos or more, and attn_get_device_status then
+ * returns ATTN_ERR_SHAPE. Without positions N <= n_pos (ATTN_ERR_SHAPE).
+ */
+ATTN_API attn_status attn_rope(const void* x, void* y, const float* rope_cos, const float* rope_sin,
+                               const int* positions, const long long* x_strides, const long long* y_strides, int B,
+                               int H, int N, int d, int rot_dim, int n_pos, int interleaved, int inverse,
+                               attn_dtype dtype, void* stream);
+
+/*
+ * The tables that attn_rope, attn_quantize_fp8_rope and attn_cache_append_fp8
+ * read: row r, pair i < rot_dim/2 of rope_cos and rope_sin (float32 [n_pos,
+ * rot_dim/2]) is amplitude * cos and amplitude * sin of the angle
+ * (first_position + r) * inv_freq[i], inv_freq float64 [rot_dim/2] on the
+ * device (radians per position; the caller's scaling for long contexts goes
+ * into inv_freq and amplitude). The angle is taken modulo one turn in 64-bit
+ * fixed point, so far positions lose nothing: the error is that of float32
+ * cosines and sines, 2e-7 amplitude. 0 <= first_position <= 2^40, rot_dim a
+ * multiple of 16 up to 256.
+ */
+ATTN_API attn_status attn_rope_tables(float* rope_cos, float* rope_sin, const double* inv_freq,
+                                      long long first_position, int n_pos, int rot_dim, float amplitude,
+                                      void* stream);
+
+/*
+ * Append new rows to a block-quantised KV cache (the operand that
+ * attn_decode_fp8 and attn_decode_cache_fp8 read), optionally rotating the
+ * keys first. k, v: new rows [B,Hkv,n_new,d] of `dtype` (BF16/FP16) with HOST
+ * arrays of element strides as attn_rope; sequence b appends its first
+ * new_lens[b] of them (int32 [B] on the device; NULL: n_new; clamped to 0 ..
+ * n_new) behind its seqlens[b] rows (int32 [B], not changed by the call).
+ * The cache is dense, k8/v8 [B,Hkv,Nmax,d] with factors sk/sv
+ * [B,Hkv,ceil(Nmax/128)], or paged where block_table is not NULL: pages of 128 rows
+ * k8/v8 [num_pages,Hkv,128,d], factors [num_pages,Hkv], block_table int32
+ * [B,Nmax/128] giving the page of each 128 rows of a sequence (Nmax a
+ * multiple of 128). Every 128-row block that gets a row then holds
+ * attn_quantize_fp8's result for its earlier rows (at the values their codes
+ * stand for) and the new ones together: where the factor moves, the earlier
+ * rows' codes are written again at the new one. Rows behind the new ones are
+ * left as they were.
+ * rope_cos, rope_sin (both or neither): tables [n_pos, rot_dim/2]; row r of
+ * a sequence has position r and its key is turned as attn_rope does, in
+ * float32, each product and sum rounded on its own, and not rounded to
+ * `dtype` before the quantisation.
+ * Rows that do not fit (past Nmax, past n_pos, in a block whose page is
+ * outside [0, num_pages), or behind a negative length) are dropped and
+ * attn_get_device_status then returns ATTN_ERR_SHAPE. A page may stand in
+ * several sequences' tables, but a page that the call writes only once.
+ * Finite inputs: an infinity or NaN spoils its block's factor. B <= 32767.
+ */
+ATTN_API attn_status attn_cache_append_fp8(const void* k, const void* v, const long long* k_strides,
+                                           const long long* v_strides, void* k8, void* v8, float* sk, float* sv,
+                                           const int* seqlens, const int* new_lens, const int* block_table,
+                                           const float* rope_cos, const float* rope_sin, int B, int Hkv, int n_new,
+                                           int Nmax, int num_pages, int d, int rot_dim, int n_pos, int interleaved,
+                                           attn_dtype dtype, void* stream);
+
+/* Splits that suit attn_decode_cache_fp8 for these sizes (blocks: ceil(Nmax /
+ * 128)): enough CTAs to fill the GPU several times over. 0 for sizes out of
+ * range. No device work. */
+ATTN_API int attn_decode_cache_fp8_splits(int B, int Hq, int Hkv, int blocks);
+
+/* Bytes of workspace attn_decode_cache_fp8 needs (that of attn_decode_fp8;
+ * 256 for one split, which needs no partial results). */
+ATTN_API size_t attn_decode_cache_fp8_workspace_size(int B, int Hq, int d, int num_splits);
+
+/*
+ * Attention of one new token per sequence over a block-quantised cache, with
+ * a 16-bit query and P kept in 16 bits (attn_decode_fp8 takes an E4M3 query
+ * and rounds P to E4M3), for a dense or paged cache (k8, v8, sk, sv,
+ * block_table, Nmax, num_pages as attn_cache_append_fp8), with the score
+ * changes of attn_fwd_score. q, o [B,Hq,d] of `dtype` (BF16/FP16), lse [B,Hq]
+ * float32. The query of sequence b stands at position L - 1, L = seqlens[b]
+ * (int32 [B] on the device, clamped to 0 .. Nmax) and sees keys j with
+ * max(0, L - 1 - window_left) <= j < L (window_left = -1: from 0):
+ *   x_j = scale q.k_j; score_cap > 0: x_j = score_cap tanh(x_j / score_cap);
+ *   slopes (float32 [Hq], or NULL): x_j -= slopes[h] (L - 1 - j);
+ *   o = sum_j softmax(x)_j v_j,  lse = log sum_j exp(x_j).
+ * A sequence of length 0 gives o = 0 and lse = -inf. Keys in a block whose
+ * page is outside [0, num_pages) are not seen, and attn_get_device_status
+ * then returns ATTN_ERR_SHAPE. What the cache holds outside the visible rows
+ * (unwritten memory included) has no influence.
+ * 1 <= num_splits <= ceil(Nmax/128): each split is a run of ceil(blocks /
+ * num_splits) blocks from the first visible one; a second kernel combines
+ * them. workspace: attn_decode_cache_fp8_workspace_size bytes; concurrent
+ * calls need workspaces of their own. score_cap negative, infinite or NaN:
+ * ATTN_ERR_SHAPE.
+ */
+ATTN_API attn_status attn_decode_cache_fp8(const void* q, const void* k8, const void* v8, const float* sk,
+                                           const float* sv, const int* block_table, const int* seqlens,
+                                           const float* slopes, void* o, float* lse, void* workspace,
+                                           size_t ws_bytes, int B, int Hq, int Hkv, int Nmax, int num_pages, int d,
+                                           float scale, float score_cap, int window_left, int num_splits,
+                                           attn_dtype dtype, void* stream);
+
 /* Bytes of device workspace attn_bwd needs: FP32 dQ accumulator [B,Hq,N,d]
  * plus D = rowsum(dO o O) [B,Hq,N], each rounded up to 256 bytes. */
 ATTN_API size_t attn_bwd_workspace_size(int B, int Hq, int Hkv, int N, int d);
@@ -340,7 +452,9 @@ ATTN_API attn_status attn_bwd_varlen(const void* q, const void* k, const void* v
 /*
  * Device status of the library's kernels on the current device: every wait
  * inside a kernel is bounded; one that runs out records ATTN_ERR_TIMEOUT in a
- * device word and the kernel returns early. This call synchronises `stream`,
+ * device word and the kernel returns early. A kernel that meets an index out
+ * of range in a device array (a position, a length, a page) skips it and
+ * records ATTN_ERR_SHAPE. This call synchronises `stream`,
  * reads the word, clears it and returns it (ATTN_OK when nothing happened).
  */
 ATTN_API attn_status attn_get_device_status(void* stream);

@@ -11,6 +11,8 @@ attention : the plain definition of scaled-dot-product attention, its
 fp8       : the E4M3 codec, power-of-two block scales, the random-sign
             Hadamard rotation and an emulation of block-quantised FP8
             attention that follows the tiled algorithm step by step.
+score     : capped and biased scores with row masks (forward, backward, single
+            tokens), rotary positions, appending to a quantised cache.
 
 Parity status: every function is pinned by ``tests/test_oracle_*.py``. For
 ``fp8.attention_fp8`` and ``fp8.decode_fp8`` everything but the E4M3 rounding
