@@ -30,7 +30,9 @@ EXPORTS = ("attn_status_string", "attn_version", "attn_fwd", "attn_fwd_varlen", 
            "attn_bwd_deterministic", "attn_quantize_fp8_rope", "attn_decode_fp8_workspace_size",
            "attn_decode_fp8", "attn_fwd_fp8_kv_tile", "attn_quantize_fp8_varlen", "attn_fwd_fp8_varlen",
            "attn_fwd_fp8_window", "attn_rope", "attn_rope_tables", "attn_cache_append_fp8",
-           "attn_decode_cache_fp8_splits", "attn_decode_cache_fp8_workspace_size", "attn_decode_cache_fp8")
+           "attn_decode_cache_fp8_splits", "attn_decode_cache_fp8_workspace_size", "attn_decode_cache_fp8",
+           "attn_mask_rows", "attn_score_workspace_size", "attn_fwd_score", "attn_bwd_score_workspace_size",
+           "attn_bwd_score")
 
 
 class AttnError(RuntimeError):
@@ -66,6 +68,11 @@ _SIGS = {
     "attn_bwd_deterministic": ([_P] * 9 + [_P, _Z, _I, _I, _I, _I, _I, _F, _I, _I, _I, _P], _I),
     "attn_quantize_fp8_varlen": ([_P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P], _I),
     "attn_fwd_fp8_varlen": ([_P] * 9 + [_I, _I, _I, _I, _I, _I, _F, _I, _P], _I),
+    "attn_mask_rows": ([_P, _P, _P, _I, _I, _I, _P], _I),
+    "attn_score_workspace_size": ([_I, _I], _Z),
+    "attn_fwd_score": ([_P] * 8 + [_Z] + [_I] * 5 + [_F, _F, _I, _I, _I, _P], _I),
+    "attn_bwd_score_workspace_size": ([_I, _I, _I, _I, _I], _Z),
+    "attn_bwd_score": ([_P] * 12 + [_Z] + [_I] * 5 + [_F, _F, _I, _I, _I, _P], _I),
     "attn_rope": ([_P] * 5 + [_S, _S] + [_I] * 9 + [_P], _I),
     "attn_rope_tables": ([_P, _P, _P, C.c_longlong, _I, _I, _F, _P], _I),
     "attn_cache_append_fp8": ([_P, _P, _S, _S] + [_P] * 9 + [_I] * 10 + [_P], _I),
@@ -368,6 +375,57 @@ def attn_rope_tables(rope_cos, rope_sin, inv_freq, first_position=0, amplitude=1
     pc, ps, rot, n_pos = _rope_dims(rope_cos, rope_sin)
     _check(load().attn_rope_tables(pc, ps, _ptr(inv_freq, "inv_freq", rot // 2, torch.float64), int(first_position),
                                    n_pos, rot, float(amplitude), _stream(stream)), "attn_rope_tables")
+
+
+def attn_mask_rows(row_ranges, doc_ids=None, prefix_lens=None, causal=True, stream=None):
+    """Visible keys [lo, hi) of every row into row_ranges int32 [B,N,2]: doc_ids int32 [B,N] (runs of
+    equal ids; negative: padding), prefix_lens int32 [B] (keys below are seen by their whole document)."""
+    B, N, _ = _dims(row_ranges, "row_ranges", 3)
+    _one_device(row_ranges, doc_ids, prefix_lens)
+    _check(load().attn_mask_rows(_ptr(doc_ids, "doc_ids", dtype=torch.int32, shape=(B, N)),
+                                 _ptr(prefix_lens, "prefix_lens", B, torch.int32),
+                                 _ptr(row_ranges, "row_ranges", dtype=torch.int32, shape=(B, N, 2)), B, N,
+                                 int(bool(causal)), _stream(stream)), "attn_mask_rows")
+
+
+def attn_score_workspace_size(B, N):
+    return load().attn_score_workspace_size(B, N)
+
+
+def attn_fwd_score(q, k, v, o, lse, workspace=None, row_ranges=None, slopes=None, score_cap=0.0, window=(-1, -1),
+                   scale=None, stream=None):
+    """Dense forward with scores cap * tanh(s / cap) - slopes[h] |i - j|, key window and row ranges
+    int32 [B,N,2] (these need a workspace of attn_score_workspace_size bytes); slopes fp32 [Hq]."""
+    B, Hq, N, d = _dims(q, "q", 4)
+    Hkv = _dims(k, "k", 4)[1]
+    _one_device(q, k, v, o, lse, workspace, row_ranges, slopes)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    left, right = (int(w) for w in window)
+    _check(load().attn_fwd_score(*_fwd_ptrs(q, k, v, o, lse),
+                                 _ptr(row_ranges, "row_ranges", dtype=torch.int32, shape=(B, N, 2)),
+                                 _ptr(slopes, "slopes", Hq, torch.float32), _ptr(workspace, "workspace"),
+                                 0 if workspace is None else workspace.numel() * workspace.element_size(), B, Hq, Hkv,
+                                 N, d, scale, float(score_cap), left, right, _dtype(q), _stream(stream)),
+           "attn_fwd_score")
+
+
+def attn_bwd_score_workspace_size(B, Hq, Hkv, N, d):
+    return load().attn_bwd_score_workspace_size(B, Hq, Hkv, N, d)
+
+
+def attn_bwd_score(q, k, v, o, lse, dout, dq, dk, dv, workspace, row_ranges=None, slopes=None, score_cap=0.0,
+                   window=(-1, -1), scale=None, stream=None):
+    """Backward of attn_fwd_score; workspace of attn_bwd_score_workspace_size bytes."""
+    B, Hq, N, d = _dims(q, "q", 4)
+    Hkv = _dims(k, "k", 4)[1]
+    _one_device(q, k, v, o, lse, dout, dq, dk, dv, workspace, row_ranges, slopes)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    left, right = (int(w) for w in window)
+    _check(load().attn_bwd_score(*_bwd_ptrs(q, k, v, o, lse, dout, dq, dk, dv),
+                                 _ptr(row_ranges, "row_ranges", dtype=torch.int32, shape=(B, N, 2)),
+                                 _ptr(slopes, "slopes", Hq, torch.float32), _ptr(workspace, "workspace"),
+                                 workspace.numel() * workspace.element_size(), B, Hq, Hkv, N, d, scale,
+                                 float(score_cap), left, right, _dtype(q), _stream(stream)), "attn_bwd_score")
 
 
 def _cache_ptrs(k8, v8, sk, sv, block_table, B, Hkv, d):

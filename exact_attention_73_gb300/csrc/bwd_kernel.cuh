@@ -53,6 +53,8 @@
 #pragma once
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
+
 #include <cuda.h>
 
 #include "fwd_kernel.cuh"
@@ -87,6 +89,7 @@ struct BwdArgs {
   // persistent instance: the grid walks units blockIdx.x, + gridDim.x, ...
   // below `units` (tiles_x * Hkv * batch), in the linear order above
   int units;
+  ScoreArgs sc;                 // kScore instances only
 };
 
 // kP: the persistent walk's layout. At d = 64 it holds two K/V buffers, so
@@ -190,7 +193,10 @@ __device__ __forceinline__ void split_add(uint32_t (&v)[32], const float* part1,
 // kDQ = false: dK and dV only (the deterministic backward computes dQ in a
 // separate query-stationary kernel); the dQ^T product, its drain and the
 // reduce-adds are left out.
-template <int DT, int D, bool kDQ = true, bool kSplit = false, bool kPersist = false>
+// kScore: scores may be capped and biased and rows masked by ranges
+// (score.cuh). dS takes the cap's derivative, 1 - tanh^2 = 1 - (x / cap)^2,
+// from the capped score itself.
+template <int DT, int D, bool kDQ = true, bool kSplit = false, bool kPersist = false, bool kScore = false>
 __global__ void __launch_bounds__(512, 1)
 bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
            const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
@@ -281,6 +287,13 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     const int qhi = a.win_left < 0 ? L - 1 : min(L - 1, klast + a.win_left);
     i0 = qlo / C::BR;
     per_head = qhi / C::BR + 1 - i0;
+    if constexpr (kScore) {
+      if (a.sc.ranges) {
+        const int2 t = __ldg(a.sc.key_tiles + static_cast<long long>(b) * ((a.N + C::BC - 1) / C::BC) + j);
+        i0 = t.x;
+        per_head = t.y - t.x;
+      }
+    }
     // this CTA's part of the walk over (query head, query tile): iterations
     // it_base .. it_base + niter - 1 of the group * per_head
     it_base = wp * (a.group * per_head) / nsplit;
@@ -650,6 +663,12 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
         const uint32_t xb = tbase + lane_off + 128u * (g & 1);
         uint8_t* ds_row = sDS + (C::NDS > 1 ? (g & 1) * C::DS_B : 0) + r * 128;
         const int st = g % C::NQ;
+        int4 bnd = make_int4(0, 0, 0, 0);   // visible keys of the tile's rows: intersection in .z, .w
+        float slope2 = 0.f;
+        if constexpr (kScore) {   // fetched before the waits, which cover the latency
+          if (a.sc.ranges) bnd = __ldg(a.sc.bounds + static_cast<long long>(b) * a.sc.ntile + q_tile(it));
+          if (a.sc.slopes) slope2 = __ldg(a.sc.slopes + q_head(it)) * kLog2e;
+        }
         // LSE and D of this stage (written by the load warp before it arrived
         // on q_full[st]) go to registers first: these shared-memory reads then
         // overlap the wait for S^T/dP^T instead of heading every exp2 chain
@@ -682,23 +701,77 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
         if (!ok) break;
         const int q0 = q_tile(it) * C::BR + 32 * half;
         // this key against queries q0 .. q0 + 31: outside the sequence or the window?
-        const bool edge = kPersist ? !kvalid
+        bool edge = kPersist ? !kvalid
                                    : !kvalid || (a.win_right >= 0 && kloc > q0 + a.win_right) ||
                                          (a.win_left >= 0 && kloc < q0 + 31 - a.win_left);
+        if constexpr (kScore) {
+          if (a.sc.ranges) edge = !kvalid || kloc < bnd.z || kloc >= bnd.w;
+          if (a.sc.cap_log2 > 0.f) {   // capped scores in place of the raw ones
+            const float big = rowmax_abs(sv);
+            if (!warp_any(!(big <= a.sc.s_small))) {
+  #pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                const float2 s2 = make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+                const float2 y = fmul2(s2, cap_small_factor(s2, a.sc));
+                sv[c] = __float_as_uint(y.x);
+                sv[c + 1] = __float_as_uint(y.y);
+              }
+            } else if (!warp_any(!(big * fabsf(a.sc.w_of_s) <= 1.f))) {
+  #pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                const float2 y = cap_pair(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), a.sc.w_of_s,
+                                          a.sc.cap_log2);
+                sv[c] = __float_as_uint(y.x);
+                sv[c + 1] = __float_as_uint(y.y);
+              }
+            } else {
+  #pragma unroll
+              for (int c = 0; c < 32; ++c)
+                sv[c] = __float_as_uint(cap_any(__uint_as_float(sv[c]), a.sc.w_of_s, a.sc.cap_log2));
+            }
+          }
+        }
         uint32_t pp[16], dd[16];
+        // kCap: sv holds capped log2 scores, and dS takes the cap's derivative
+        auto weights = [&](auto cap) {
+          constexpr bool kCap = decltype(cap)::value;
   #pragma unroll
         for (int e4 = 0; e4 < 8; ++e4) {
-          const float4 l4 = l4r[e4];
+          float4 l4 = l4r[e4];
           const float4 d4 = d4r[e4];
-          float2 x01 = ffma2(make_float2(__uint_as_float(sv[4 * e4]), __uint_as_float(sv[4 * e4 + 1])), sl2v,
-                             make_float2(l4.x, l4.y));
-          float2 x23 = ffma2(make_float2(__uint_as_float(sv[4 * e4 + 2]), __uint_as_float(sv[4 * e4 + 3])), sl2v,
-                             make_float2(l4.z, l4.w));
+          if constexpr (kScore) {
+            if (a.sc.slopes) {   // the bias joins -LSE
+              const float from = static_cast<float>(q0 + 4 * e4 - kloc);
+              l4.x = fmaf(-slope2, fabsf(from), l4.x);
+              l4.y = fmaf(-slope2, fabsf(from + 1.f), l4.y);
+              l4.z = fmaf(-slope2, fabsf(from + 2.f), l4.z);
+              l4.w = fmaf(-slope2, fabsf(from + 3.f), l4.w);
+            }
+          }
+          const float2 s01 = make_float2(__uint_as_float(sv[4 * e4]), __uint_as_float(sv[4 * e4 + 1]));
+          const float2 s23 = make_float2(__uint_as_float(sv[4 * e4 + 2]), __uint_as_float(sv[4 * e4 + 3]));
+          float2 x01, x23;
+          if constexpr (kCap) {
+            x01 = fadd2(s01, make_float2(l4.x, l4.y));
+            x23 = fadd2(s23, make_float2(l4.z, l4.w));
+          } else {
+            x01 = ffma2(s01, sl2v, make_float2(l4.x, l4.y));
+            x23 = ffma2(s23, sl2v, make_float2(l4.z, l4.w));
+          }
           float p[4] = {ex2(x01.x), ex2(x01.y), ex2(x23.x), ex2(x23.y)};
           if (edge) {
   #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const int q = q0 + 4 * e4 + u;
+              if constexpr (kScore) {
+                if (a.sc.ranges) {
+                  const int2 r = q < L ? score_row(a.sc.ranges, static_cast<long long>(b) * L + q, q, L, a.win_left,
+                                                   a.win_right)
+                                       : make_int2(L, 0);
+                  if (kloc < r.x || kloc >= r.y) p[u] = 0.f;
+                  continue;
+                }
+              }
               if (!kvalid || (a.win_right >= 0 && kloc > q + a.win_right) || (a.win_left >= 0 && kloc < q - a.win_left))
                 p[u] = 0.f;
             }
@@ -707,8 +780,14 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                                    make_float2(d4.x, d4.y));
           const float2 t23 = fadd2(make_float2(__uint_as_float(dp[4 * e4 + 2]), __uint_as_float(dp[4 * e4 + 3])),
                                    make_float2(d4.z, d4.w));
-          const float2 g01 = fmul2(make_float2(p[0], p[1]), t01);
-          const float2 g23 = fmul2(make_float2(p[2], p[3]), t23);
+          float2 g01 = fmul2(make_float2(p[0], p[1]), t01);
+          float2 g23 = fmul2(make_float2(p[2], p[3]), t23);
+          if constexpr (kCap) {
+            const float2 c2 = make_float2(a.sc.inv_cap2, a.sc.inv_cap2), one = make_float2(1.f, 1.f);
+            const float2 t0 = fmul2(s01, c2), t1 = fmul2(s23, c2);   // tanh
+            g01 = fmul2(g01, ffma2(make_float2(-t0.x, -t0.y), t0, one));
+            g23 = fmul2(g23, ffma2(make_float2(-t1.x, -t1.y), t1, one));
+          }
           if constexpr (DT == kBF16) {
             pp[2 * e4] = pack_bf16x2(p[0], p[1]);
             pp[2 * e4 + 1] = pack_bf16x2(p[2], p[3]);
@@ -720,6 +799,13 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
             dd[2 * e4] = pack_f16x2(g01.x, g01.y);
             dd[2 * e4 + 1] = pack_f16x2(g23.x, g23.y);
           }
+        }
+        };
+        if constexpr (kScore) {
+          if (a.sc.cap_log2 > 0.f) weights(std::true_type{});
+          else weights(std::false_type{});
+        } else {
+          weights(std::false_type{});
         }
         tmem_st16(xb + C::col_p(2 * half), pp);
         tmem_st16(xb + C::col_ds(2 * half), dd);

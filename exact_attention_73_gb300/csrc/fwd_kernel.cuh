@@ -27,11 +27,14 @@
 #pragma once
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
+
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "ptx.cuh"
+#include "score.cuh"
 
 namespace attn {
 
@@ -62,6 +65,7 @@ struct FwdArgs {
   // fwd_kernel: units of QT query tiles, ux query-tile groups x uy query
   // heads x uz batches (or packed sequences); the grid walks them.
   int ux, uy, uz;
+  ScoreArgs sc;                 // kScore instances only
 };
 
 template <int DT, int D, int QT>
@@ -154,7 +158,7 @@ __device__ __forceinline__ int fwd_unit_of(const FwdArgs& a, int k) {
 
 // Decode unit `lin`; false when it holds no query row (a packed sequence
 // shorter than the longest one).
-template <int QT>
+template <int QT, bool kScore = false>
 __device__ __forceinline__ bool fwd_unit(const FwdArgs& a, int lin, FwdUnit& w) {
   int bx, by, bz;
   if (a.causal) {
@@ -183,8 +187,23 @@ __device__ __forceinline__ bool fwd_unit(const FwdArgs& a, int lin, FwdUnit& w) 
   if (w.qt0 >= w.nqt) return false;
   // KV tiles that hold a key visible to some query row of the unit
   const int r0 = w.qt0 * 128, r1 = min((w.qt0 + QT) * 128, w.L);
-  const int klo = a.win_left < 0 ? 0 : max(0, r0 - a.win_left);
-  const int khi = a.win_right < 0 ? w.L : min(w.L, r1 + a.win_right);   // exclusive
+  int klo = a.win_left < 0 ? 0 : max(0, r0 - a.win_left);
+  int khi = a.win_right < 0 ? w.L : min(w.L, r1 + a.win_right);   // exclusive
+  if constexpr (kScore) {
+    if (a.sc.ranges) {   // the union over the unit's 64-row tiles; rows that see nothing get one masked tile
+      klo = w.L;
+      khi = 0;
+      for (int i = w.qt0 * 2; i < min((w.qt0 + QT) * 2, a.sc.ntile); ++i) {
+        const int4 t = __ldg(a.sc.bounds + static_cast<long long>(w.b) * a.sc.ntile + i);
+        klo = min(klo, t.x);
+        khi = max(khi, t.y);
+      }
+      if (klo >= khi) {
+        klo = 0;
+        khi = 1;
+      }
+    }
+  }
   w.kv0 = klo >> 7;
   w.nkv = ((khi + 127) >> 7) - w.kv0;
   w.hkv = w.h / a.group;
@@ -195,7 +214,8 @@ __device__ __forceinline__ bool fwd_unit(const FwdArgs& a, int lin, FwdUnit& w) 
 // kPersist: the grid is smaller than the unit count and each CTA walks its
 // units; otherwise every CTA takes one unit and the unit loops below run
 // once (known at compile time, so their bookkeeping folds away).
-template <int DT, int D, int QT, bool kPersist>
+// kScore: scores may be capped and biased and rows masked by ranges (score.cuh).
+template <int DT, int D, int QT, bool kPersist, bool kScore = false>
 __global__ void __launch_bounds__(FwdCfg<DT, D, QT>::NTHREADS, 1)
 fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
            const __grid_constant__ CUtensorMap tmV, const FwdArgs a) {
@@ -224,7 +244,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     for (int k = 0; !any; ++k) {
       const int lin = fwd_unit_of(a, k);
       if (lin < 0) break;
-      any = fwd_unit<QT>(a, lin, w);
+      any = fwd_unit<QT, kScore>(a, lin, w);
     }
     if (!any) return;
   }
@@ -275,7 +295,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         const int lin = fwd_unit_of(a, k);
         if (lin < 0) break;
         FwdUnit w;
-        if (!fwd_unit<QT>(a, lin, w)) continue;
+        if (!fwd_unit<QT, kScore>(a, lin, w)) continue;
         // K/V tile `it` of this unit into the ring
         auto load_kv = [&](int it) {
           const int slot = (kvit + it) % C::NSLOT;
@@ -353,7 +373,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         const int lin = fwd_unit_of(a, k);
         if (lin < 0) break;
         FwdUnit w;
-        if (!fwd_unit<QT>(a, lin, w)) continue;
+        if (!fwd_unit<QT, kScore>(a, lin, w)) continue;
         nkv = w.nkv;
         ok = mbar_wait(q_full, ui & 1, a.status) && kv_wait(0);
         if constexpr (QT == 1) {
@@ -449,12 +469,19 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       const int lin = fwd_unit_of(a, k);
       if (lin < 0) break;
       FwdUnit w;
-      if (!fwd_unit<QT>(a, lin, w)) continue;
+      if (!fwd_unit<QT, kScore>(a, lin, w)) continue;
       const int nkv = w.nkv, L = w.L, kv0 = w.kv0;
       const int qtile = w.qt0 + t;
       const int qrow = qtile * 128 + row;
       float m = -INFINITY;     // running max of x = S * scale * log2(e)
       float l = 0.f;           // running sum of exp2(x - m)
+      int2 vis = make_int2(0, L);   // kScore: this row's visible keys
+      float slope2 = 0.f;
+      if constexpr (kScore) {
+        if (qrow < L)
+          vis = score_row(a.sc.ranges, static_cast<long long>(w.b) * L + qrow, qrow, L, a.win_left, a.win_right);
+        if (a.sc.slopes) slope2 = __ldg(a.sc.slopes + w.h) * 1.4426950408889634f;
+      }
       int f_run = -1000;       // FP8: running max exponent of the V factors
       float q_fac = 1.f;
       long long vs_base = 0;
@@ -493,11 +520,66 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         for (int c = 0; c < 4; ++c) reg_fence(*reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
         const int kb = (kv0 + j) * 128;
         // mask keys past the sequence and outside the window [qrow - left, qrow + right]
-        if (kb + 128 > L || (a.win_right >= 0 && kb + 127 > qtile * 128 + a.win_right) ||
-            (a.win_left >= 0 && kb < qtile * 128 + 127 - a.win_left)) {
-          int hi = L - kb;                                             // visible: lo <= c < hi
-          if (a.win_right >= 0) hi = min(hi, qrow + a.win_right - kb + 1);
-          const int lo = a.win_left >= 0 ? qrow - a.win_left - kb : 0;
+        bool edge;
+        if constexpr (kScore) {
+          edge = warp_any(vis.x > kb || vis.y < kb + 128);
+        } else {
+          edge = kb + 128 > L || (a.win_right >= 0 && kb + 127 > qtile * 128 + a.win_right) ||
+                 (a.win_left >= 0 && kb < qtile * 128 + 127 - a.win_left);
+        }
+        // kScore: a capped tile with small scores, no bias and no mask keeps
+        // its raw scores; tanh is folded into the exponent below. Otherwise
+        // the scores become their final log2 values here.
+        bool fused = false, final_scores = false;
+        if constexpr (kScore) {
+          if (a.sc.cap_log2 > 0.f || a.sc.slopes) {
+            float big = 0.f;
+            if (a.sc.cap_log2 > 0.f) big = rowmax_abs(sr);
+            fused = a.sc.cap_log2 > 0.f && !a.sc.slopes && !edge && !warp_any(!(big <= a.sc.s_small));
+            if (!fused) {
+              final_scores = true;
+              if (a.sc.cap_log2 > 0.f) {
+                if (!warp_any(!(big * fabsf(a.sc.w_of_s) <= 1.f))) {
+#pragma unroll
+                  for (int c = 0; c < 128; c += 2) {
+                    const float2 y = cap_pair(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
+                                              a.sc.w_of_s, a.sc.cap_log2);
+                    sr[c] = __float_as_uint(y.x);
+                    sr[c + 1] = __float_as_uint(y.y);
+                  }
+                } else {
+#pragma unroll
+                  for (int c = 0; c < 128; ++c)
+                    sr[c] = __float_as_uint(cap_any(__uint_as_float(sr[c]), a.sc.w_of_s, a.sc.cap_log2));
+                }
+              } else {
+                const float2 f = make_float2(a.sc.sl2, a.sc.sl2);
+#pragma unroll
+                for (int c = 0; c < 128; c += 2) {
+                  const float2 y = fmul2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), f);
+                  sr[c] = __float_as_uint(y.x);
+                  sr[c + 1] = __float_as_uint(y.y);
+                }
+              }
+              if (a.sc.slopes) {
+                const float from = static_cast<float>(kb - qrow);   // key - row of column 0
+#pragma unroll
+                for (int c = 0; c < 128; ++c)
+                  sr[c] = __float_as_uint(fmaf(-slope2, fabsf(from + static_cast<float>(c)), __uint_as_float(sr[c])));
+              }
+            }
+          }
+        }
+        if (edge) {
+          int hi, lo;                                                  // visible: lo <= c < hi
+          if constexpr (kScore) {
+            lo = vis.x - kb;
+            hi = vis.y - kb;
+          } else {
+            hi = L - kb;
+            if (a.win_right >= 0) hi = min(hi, qrow + a.win_right - kb + 1);
+            lo = a.win_left >= 0 ? qrow - a.win_left - kb : 0;
+          }
 #pragma unroll
           for (int c = 0; c < 128; ++c)
             if (c >= hi || c < lo) sr[c] = __float_as_uint(-INFINITY);
@@ -510,7 +592,15 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
           f_j = pow2_exponent_of(sv_j);
           f_new = max(f_run, f_j);
         }
-        const float mxs = mx * sl2;
+        float mxs = mx * sl2;
+        if constexpr (kScore) {
+          if (final_scores) {
+            sl2 = 1.f;
+            mxs = mx;
+          } else if (fused) {   // tanh rises: the largest score is that of the largest raw one
+            mxs = mx * cap_small_factor(make_float2(mx, mx), a.sc).x;
+          }
+        }
         const float m_new = (mxs > m + C::kTau) ? mxs : m;
         float corr = 1.f;
         if (m_new != m) corr = ex2(m - m_new);   // m = -inf gives 0
@@ -560,18 +650,30 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             tmem_st8(tS + 8 * c, pk);
           }
         } else {
+          // kCap: the exponent is s times the degree 7 polynomial in s^2
+          auto weights = [&](auto cap) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
+            for (int c = 0; c < 4; ++c) {
+              uint32_t pk[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int i = 32 * c + 2 * e;
-              float2 x = ffma2(make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), sl2v, biasv);
-              x = make_float2(ex2(x.x), ex2(x.y));
-              acc[e & 3] = fadd2(acc[e & 3], x);
-              pk[e] = (DT == kBF16) ? pack_bf16x2(x.x, x.y) : pack_f16x2(x.x, x.y);
+              for (int e = 0; e < 16; ++e) {
+                const int i = 32 * c + 2 * e;
+                const float2 sp = make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
+                float2 f = sl2v;
+                if constexpr (decltype(cap)::value) f = cap_small_factor(sp, a.sc);
+                float2 x = ffma2(sp, f, biasv);
+                x = make_float2(ex2(x.x), ex2(x.y));
+                acc[e & 3] = fadd2(acc[e & 3], x);
+                pk[e] = (DT == kBF16) ? pack_bf16x2(x.x, x.y) : pack_f16x2(x.x, x.y);
+              }
+              tmem_st16(tS + 16 * c, pk);
             }
-            tmem_st16(tS + 16 * c, pk);
+          };
+          if constexpr (kScore) {
+            if (fused) weights(std::true_type{});
+            else weights(std::false_type{});
+          } else {
+            weights(std::false_type{});
           }
         }
         const float2 a01 = fadd2(acc[0], acc[1]), a23 = fadd2(acc[2], acc[3]);
@@ -594,6 +696,9 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       tc_fence_after();
       if (!ok) break;
       float inv = 1.f / l;
+      if constexpr (kScore) {
+        if (l == 0.f) inv = 0.f;   // the row sees nothing: O = 0, LSE = -inf
+      }
       if constexpr (C::kFp8) inv *= exp2i(f_run - C::kPShift);
       const bool valid = qrow < L;
       const long long row_off = static_cast<long long>(w.b) * a.o_sb + static_cast<long long>(w.h) * a.o_sh +

@@ -20,16 +20,16 @@ inline bool fwd_persistent(int qt, const FwdArgs& a, int rows) {
   return a.win_left >= 0 && a.win_right >= 0 && a.win_left + a.win_right + 256 <= kFwdPersistMaxRows;
 }
 
-template <int DT, int D, int QT, bool kPersist>
+template <int DT, int D, int QT, bool kPersist, bool kScore = false>
 cudaError_t launch_fwd_grid(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const FwdArgs& u,
                             long long units, cudaStream_t st) {
   using C = FwdCfg<DT, D, QT>;
-  auto kern = fwd_kernel<DT, D, QT, kPersist>;
-  cudaError_t e = smem_attr_once<fwd_kernel<DT, D, QT, kPersist>>(C::SMEM_BYTES);
+  auto kern = fwd_kernel<DT, D, QT, kPersist, kScore>;
+  cudaError_t e = smem_attr_once<fwd_kernel<DT, D, QT, kPersist, kScore>>(C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   if constexpr (QT >= 2) {   // the role split must fit the registers of the launch
     constexpr int kSplit = (128 * C::kRegsCtl + 128 * QT * C::kRegsSoft + C::NTHREADS - 1) / C::NTHREADS;
-    if ((e = reg_pool_once<fwd_kernel<DT, D, QT, kPersist>>(C::NTHREADS, kSplit)) != cudaSuccess) return e;
+    if ((e = reg_pool_once<fwd_kernel<DT, D, QT, kPersist, kScore>>(C::NTHREADS, kSplit)) != cudaSuccess) return e;
   }
   long long grid = units;
   if (kPersist) {
@@ -55,6 +55,19 @@ cudaError_t launch_fwd_inst(const CUtensorMap& q, const CUtensorMap& k, const CU
     if (fwd_persistent(QT, a, rows)) return launch_fwd_grid<DT, D, QT, true>(q, k, v, u, units, st);
   }
   return launch_fwd_grid<DT, D, QT, false>(q, k, v, u, units, st);
+}
+
+// Score-modified instance (score.cuh): one unit per CTA.
+template <int DT, int D, int QT>
+cudaError_t launch_fwd_score_inst(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const FwdArgs& a,
+                                  int rows, int gy, int gz, cudaStream_t st) {
+  FwdArgs u = a;
+  u.ux = (rows + 128 * QT - 1) / (128 * QT);
+  u.uy = gy;
+  u.uz = gz;
+  const long long units = static_cast<long long>(u.ux) * gy * gz;
+  if (units > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_fwd_grid<DT, D, QT, false, true>(q, k, v, u, units, st);
 }
 
 }  // namespace attn

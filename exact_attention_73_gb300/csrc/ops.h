@@ -38,6 +38,10 @@ bool accum_map(CUtensorMap* m, const float* base, int d, bool packed, int B, int
 // (the box of its map).
 int bwd_dq_rows(int d);
 int bwd_dq_dims(int d);
+// Score-modified main kernel (BwdArgs::sc set), dense.
+cudaError_t launch_bwd_score(int dt, int d, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
+                             const CUtensorMap& dout, const CUtensorMap& dq_acc, const BwdArgs& a, int N, int nz,
+                             cudaStream_t st);
 cudaError_t launch_bwd_dkdv(int dt, int d, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
                             const CUtensorMap& dout, const BwdArgs& a, int max_len, int nz, cudaStream_t st);
 cudaError_t launch_bwd_dq(int dt, int d, const CUtensorMap& q, const CUtensorMap& dout, const CUtensorMap& k,

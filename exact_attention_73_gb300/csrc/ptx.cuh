@@ -441,5 +441,19 @@ __device__ __forceinline__ float rowmax(const uint32_t (&v)[N]) {
     for (int i = 0; i < 8; ++i) m[i] = fmax3(m[i], __uint_as_float(v[c + 2 * i]), __uint_as_float(v[c + 2 * i + 1]));
   return fmax3(fmax3(m[0], m[1], m[2]), fmax3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
 }
+// Largest magnitude of the same values.
+template <int N>
+__device__ __forceinline__ float rowmax_abs(const uint32_t (&v)[N]) {
+  static_assert(N % 16 == 0, "row chunk must be a multiple of 16");
+  float m[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m[i] = fmaxf(fabsf(__uint_as_float(v[2 * i])), fabsf(__uint_as_float(v[2 * i + 1])));
+#pragma unroll
+  for (int c = 16; c < N; c += 16)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      m[i] = fmax3(m[i], fabsf(__uint_as_float(v[c + 2 * i])), fabsf(__uint_as_float(v[c + 2 * i + 1])));
+  return fmax3(fmax3(m[0], m[1], m[2]), fmax3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
+}
 
 }  // namespace attn

@@ -1,0 +1,336 @@
+// Score-modified attention: the row masks, the tile facts the attention
+// kernels read, and the entry points.
+//
+// attn_mask_rows. A document is a maximal run of equal ids, so a row needs the
+// nearest change of id on either side of it. A CTA takes 1024 rows: thread-
+// local first and last changes, a max scan forward and a min scan backward
+// over the threads, and for a run that crosses the CTA's ends a search over
+// the neighbouring ids, all threads at a time (a CTA reads at most the run).
+// Four bytes in and eight out per row.
+//
+// Tile facts. Per 64 rows the union and the intersection of the rows' visible
+// keys: the forward takes the union as its KV range, both kernels skip the
+// mask where a tile lies inside the intersection. Per 128 keys the 64-row
+// tiles that see one of them: the backward's walk.
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/libattn.h"
+#include "bwd_kernel.cuh"
+#include "internal.h"
+#include "ops.h"
+
+namespace attn {
+
+namespace {
+
+constexpr int kMaskRows = 1024;   // rows per CTA, four per thread
+
+__global__ void __launch_bounds__(256) mask_rows_kernel(const int* __restrict__ ids, const int* __restrict__ prefix,
+                                                        int2* __restrict__ ranges, int N, int causal) {
+  __shared__ int red[2][8];
+  __shared__ int edge[2];
+  const int b = blockIdx.y, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int c0 = blockIdx.x * kMaskRows, c1 = min(c0 + kMaskRows, N);
+  const int r0 = c0 + 4 * t;
+  int start[4], end[4], id[4];
+  if (ids) {
+    ids += static_cast<long long>(b) * N;
+    // start of the run that reaches back over c0 - 1, end of the one that goes on past c1
+    if (t < 2) edge[t] = t == 0 ? c0 : c1;
+    __syncthreads();
+    const int first = ids[c0], last = ids[c1 - 1];
+    for (int hi = c0; hi > 0; hi -= 256) {   // rows hi - 256 .. hi - 1
+      const int r = hi - 1 - t;
+      const int differs = r >= 0 && ids[r] != first;
+      const int any = __syncthreads_or(differs);
+      if (any) {
+        if (t == 0) edge[0] = 0;
+        __syncthreads();
+        if (differs) atomicMax(&edge[0], r + 1);
+        break;
+      }
+      if (t == 0) edge[0] = max(hi - 256, 0);
+    }
+    __syncthreads();
+    for (int lo = c1; lo < N; lo += 256) {
+      const int r = lo + t;
+      const int differs = r < N && ids[r] != last;
+      const int any = __syncthreads_or(differs);
+      if (any) {
+        if (t == 0) edge[1] = N;
+        __syncthreads();
+        if (differs) atomicMin(&edge[1], r);
+        break;
+      }
+      if (t == 0) edge[1] = min(lo + 256, N);
+    }
+    __syncthreads();
+    const int edge_lo = edge[0], edge_hi = edge[1];
+    // changes inside the CTA's rows: row r starts a run if its id differs from row r - 1's
+    int s = -1, e = INT_MAX;                  // last start of this thread's rows, first end
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = r0 + u;
+      id[u] = r < c1 ? ids[r] : 0;
+      const bool starts = r < c1 && r > c0 && ids[r - 1] != id[u];
+      if (starts) s = r;
+      start[u] = s;
+    }
+#pragma unroll
+    for (int u = 3; u >= 0; --u) {
+      const int r = r0 + u;
+      if (r < c1 - 1 && ids[r + 1] != id[u]) e = r + 1;
+      end[u] = e;
+    }
+    // scans over the threads: the last start before, the first end behind
+    int ps = s, pe = e;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, ps, o), z = __shfl_down_sync(0xffffffffu, pe, o);
+      if (lane >= o) ps = max(ps, a);
+      if (lane < 32 - o) pe = min(pe, z);
+    }
+    __syncthreads();
+    if (lane == 31) red[0][warp] = ps;
+    if (lane == 0) red[1][warp] = pe;
+    __syncthreads();
+    int before = __shfl_up_sync(0xffffffffu, ps, 1), behind = __shfl_down_sync(0xffffffffu, pe, 1);
+    if (lane == 0) before = -1;
+    if (lane == 31) behind = INT_MAX;
+    for (int w = 0; w < warp; ++w) before = max(before, red[0][w]);
+    for (int w = warp + 1; w < 8; ++w) behind = min(behind, red[1][w]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      start[u] = max(start[u], before);
+      if (start[u] < 0) start[u] = edge_lo;
+      end[u] = min(end[u], behind);
+      if (end[u] == INT_MAX) end[u] = edge_hi;
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      id[u] = 0;
+      start[u] = 0;
+      end[u] = N;
+    }
+  }
+  const int pre = prefix ? prefix[b] : 0;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int r = r0 + u;
+    if (r >= c1) break;
+    int2 v = make_int2(start[u], end[u]);
+    if (causal) v.y = max(r + 1, min(end[u], pre));
+    if (id[u] < 0) v = make_int2(0, 0);
+    ranges[static_cast<long long>(b) * N + r] = v;
+  }
+}
+
+// One warp per 64 rows.
+__global__ void __launch_bounds__(256) score_bounds_kernel(const int2* __restrict__ ranges, int4* __restrict__ bounds,
+                                                           int N, int ntile, int left, int right) {
+  const int i = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, b = blockIdx.y;
+  if (i >= ntile) return;
+  int4 v = make_int4(N, 0, 0, N);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int r = i * 64 + lane + 32 * u;
+    if (r >= N) continue;
+    const int2 s = score_row(ranges, static_cast<long long>(b) * N + r, r, N, left, right);   // (N, 0) if empty
+    v.x = min(v.x, s.x);
+    v.y = max(v.y, s.y);
+    v.z = max(v.z, s.x);
+    v.w = min(v.w, s.y);
+  }
+  v.x = __reduce_min_sync(0xffffffffu, v.x);
+  v.y = __reduce_max_sync(0xffffffffu, v.y);
+  v.z = __reduce_max_sync(0xffffffffu, v.z);
+  v.w = __reduce_min_sync(0xffffffffu, v.w);
+  if (lane == 0) bounds[static_cast<long long>(b) * ntile + i] = v;
+}
+
+// One warp per 128 keys: the first and last 64-row tile with a row that may see one.
+__global__ void __launch_bounds__(256) score_key_tiles_kernel(const int4* __restrict__ bounds, int2* __restrict__ key_tiles,
+                                                              int ntile, int nkey) {
+  const int j = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, b = blockIdx.y;
+  if (j >= nkey) return;
+  int lo = ntile, hi = 0;
+  for (int i = lane; i < ntile; i += 32) {
+    const int4 v = bounds[static_cast<long long>(b) * ntile + i];
+    if (v.x < (j + 1) * 128 && v.y > j * 128) {
+      lo = min(lo, i);
+      hi = max(hi, i + 1);
+    }
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lo >= hi) {   // keys that nobody sees: one tile, all of it masked, writes their zero gradients
+    lo = 0;
+    hi = 1;
+  }
+  if (lane == 0) key_tiles[static_cast<long long>(b) * nkey + j] = make_int2(lo, hi);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+int ntiles(int N) { return static_cast<int>((static_cast<long long>(N) + 63) / 64); }
+int nkeys(int N) { return static_cast<int>((static_cast<long long>(N) + 127) / 128); }
+
+// Arguments both directions share. `ws` holds the tile facts (row_ranges given).
+attn_status check_score(const int* row_ranges, const float* slopes, float scale, float cap, int N, int left, int right) {
+  if ((row_ranges && !aligned16(row_ranges)) || (slopes && !aligned16(slopes))) return ATTN_ERR_ALIGN;
+  if (left < -1 || right < -1 || N > (1 << 24)) return ATTN_ERR_SHAPE;   // distances are exact in float32
+  // the running max follows the largest q.k, and a masked score is -inf times the scale: scale > 0
+  if (!(cap >= 0.f) || std::isinf(cap) || !(scale > 0.f) || std::isinf(scale)) return ATTN_ERR_SHAPE;
+  return ATTN_OK;
+}
+
+cudaError_t prepare_score(ScoreArgs& a, const int* row_ranges, const float* slopes, float scale, float cap, int B,
+                          int N, int left, int right, void* facts, bool keys, cudaStream_t st) {
+  set_cap(a, scale, cap);
+  a.slopes = slopes;
+  a.ntile = ntiles(N);
+  if (!row_ranges) return cudaSuccess;
+  a.ranges = reinterpret_cast<const int2*>(row_ranges);
+  int4* bounds = static_cast<int4*>(facts);
+  a.bounds = bounds;
+  score_bounds_kernel<<<dim3((a.ntile + 7) / 8, B), 256, 0, st>>>(a.ranges, bounds, N, a.ntile, left, right);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !keys) return e;
+  int2* kt = reinterpret_cast<int2*>(bounds + static_cast<size_t>(B) * a.ntile);
+  a.key_tiles = kt;
+  score_key_tiles_kernel<<<dim3((nkeys(N) + 7) / 8, B), 256, 0, st>>>(bounds, kt, a.ntile, nkeys(N));
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" attn_status attn_mask_rows(const int* doc_ids, const int* prefix_lens, int* row_ranges, int B, int N,
+                                      int causal, void* stream) {
+  if (!row_ranges) return ATTN_ERR_NULL;
+  if (!aligned16(row_ranges) || (doc_ids && !aligned16(doc_ids)) || (prefix_lens && !aligned16(prefix_lens)))
+    return ATTN_ERR_ALIGN;
+  if (B < 1 || B > 65535 || N < 1 || N > (1 << 24)) return ATTN_ERR_SHAPE;
+  int* status;
+  attn_status s = device_context(&status);
+  if (s != ATTN_OK) return s;
+  mask_rows_kernel<<<dim3((N + kMaskRows - 1) / kMaskRows, B), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+      doc_ids, prefix_lens, reinterpret_cast<int2*>(row_ranges), N, causal ? 1 : 0);
+  return launch_status(cudaGetLastError());
+}
+
+extern "C" size_t attn_score_workspace_size(int B, int N) {
+  if (B < 1 || N < 1) return 0;
+  return round256(static_cast<size_t>(B) * (ntiles(N) * sizeof(int4) + nkeys(N) * sizeof(int2)));
+}
+
+extern "C" attn_status attn_fwd_score(const void* q, const void* k, const void* v, void* o, float* lse,
+                                      const int* row_ranges, const float* slopes, void* workspace, size_t ws_bytes,
+                                      int B, int Hq, int Hkv, int N, int d, float scale, float score_cap,
+                                      int window_left, int window_right, attn_dtype dtype, void* stream) {
+  if (!q || !k || !v || !o || !lse || (row_ranges && !workspace)) return ATTN_ERR_NULL;
+  const void* ptrs[] = {q, k, v, o, lse, workspace};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return ATTN_ERR_ALIGN;
+  if (B < 1 || B > 65535 || N < 1 || Hq < 1 || Hkv < 1 || Hq > 65535) return ATTN_ERR_SHAPE;
+  attn_status s = check_score(row_ranges, slopes, scale, score_cap, N, window_left, window_right);
+  if (s != ATTN_OK) return s;
+  if (d != 64 && d != 128 && d != 256) return ATTN_ERR_HEADDIM;
+  if (Hq % Hkv) return ATTN_ERR_GQA;
+  if (dtype != ATTN_BF16 && dtype != ATTN_FP16) return ATTN_ERR_DTYPE;
+  if (row_ranges && ws_bytes < attn_score_workspace_size(B, N)) return ATTN_ERR_WORKSPACE;
+  int* status;
+  if ((s = device_context(&status)) != ATTN_OK) return s;
+  CUtensorMap tq, tk, tv;
+  if (!operand_map(&tq, q, dtype, d, false, B, Hq, N, 128) || !operand_map(&tk, k, dtype, d, false, B, Hkv, N, 128) ||
+      !operand_map(&tv, v, dtype, d, false, B, Hkv, N, 128))
+    return ATTN_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  window_left = window_left < N ? window_left : N;   // wider windows bound nothing (and would overflow positions)
+  window_right = window_right < N ? window_right : N;
+  FwdArgs a{};
+  a.o = o;
+  a.lse = lse;
+  a.o_sn = d;
+  a.o_sh = static_cast<long long>(N) * d;
+  a.o_sb = static_cast<long long>(Hq) * N * d;
+  a.l_sh = N;
+  a.l_sb = static_cast<long long>(Hq) * N;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.group = Hq / Hkv;
+  a.N = N;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.win_left = window_left;
+  a.win_right = window_right;
+  a.causal = !row_ranges && window_left < 0 && window_right == 0 ? 1 : 0;
+  a.status = status;
+  cudaError_t e = prepare_score(a.sc, row_ranges, slopes, scale, score_cap, B, N, window_left, window_right, workspace,
+                                false, st);
+  if (e == cudaSuccess)
+    e = dtype == ATTN_BF16 ? launch_fwd_score_bf16(d, tq, tk, tv, a, N, Hq, B, st)
+                           : launch_fwd_score_fp16(d, tq, tk, tv, a, N, Hq, B, st);
+  return launch_status(e);
+}
+
+extern "C" size_t attn_bwd_score_workspace_size(int B, int Hq, int Hkv, int N, int d) {
+  const size_t base = attn_bwd_workspace_size(B, Hq, Hkv, N, d);
+  return base == 0 ? 0 : base + attn_score_workspace_size(B, N);
+}
+
+extern "C" attn_status attn_bwd_score(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                                      const void* dout, void* dq, void* dk, void* dv, const int* row_ranges,
+                                      const float* slopes, void* workspace, size_t ws_bytes, int B, int Hq, int Hkv,
+                                      int N, int d, float scale, float score_cap, int window_left, int window_right,
+                                      attn_dtype dtype, void* stream) {
+  attn_status s = bwd_check_dense(q, k, v, o, lse, dout, dq, dk, dv, workspace, ws_bytes, B, Hq, Hkv, N, d, dtype);
+  if (s != ATTN_OK) return s;
+  if ((s = check_score(row_ranges, slopes, scale, score_cap, N, window_left, window_right)) != ATTN_OK) return s;
+  if (ws_bytes < attn_bwd_score_workspace_size(B, Hq, Hkv, N, d)) return ATTN_ERR_WORKSPACE;
+  int* status;
+  if ((s = device_context(&status)) != ATTN_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  window_left = window_left < N ? window_left : N;
+  window_right = window_right < N ? window_right : N;
+  const size_t rows = static_cast<size_t>(B) * Hq * N;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* dq_acc = reinterpret_cast<float*>(ws);
+  float* dvec = reinterpret_cast<float*>(ws + round256(rows * d * 4));
+  void* facts = ws + attn_bwd_workspace_size(B, Hq, Hkv, N, d);
+  CUtensorMap tk, tv, tq, tdo, tdq;
+  if (!operand_map(&tk, k, dtype, d, false, B, Hkv, N, 128) || !operand_map(&tv, v, dtype, d, false, B, Hkv, N, 128) ||
+      !operand_map(&tq, q, dtype, d, false, B, Hq, N, 64) || !operand_map(&tdo, dout, dtype, d, false, B, Hq, N, 64) ||
+      !accum_map(&tdq, dq_acc, d, false, B, Hq, N, bwd_dq_rows(d), bwd_dq_dims(d)))
+    return ATTN_ERR_CUDA;
+  BwdArgs a{};
+  a.lse = lse;
+  a.dvec = dvec;
+  a.dq_acc = dq_acc;
+  a.dk = dk;
+  a.dv = dv;
+  a.q_sn = d; a.q_sh = static_cast<long long>(N) * d; a.q_sb = static_cast<long long>(Hq) * N * d;
+  a.k_sn = d; a.k_sh = static_cast<long long>(N) * d; a.k_sb = static_cast<long long>(Hkv) * N * d;
+  a.l_sh = N; a.l_sb = static_cast<long long>(Hq) * N;
+  a.N = N;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.group = Hq / Hkv;
+  a.scale = scale;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.win_left = window_left;
+  a.win_right = window_right;
+  a.causal = !row_ranges && window_left < 0 && window_right == 0 ? 1 : 0;
+  a.status = status;
+  cudaError_t e = prepare_score(a.sc, row_ranges, slopes, scale, score_cap, B, N, window_left, window_right, facts, true,
+                                st);
+  if (e == cudaSuccess) e = launch_bwd_pre(dtype, d, o, dout, dvec, dq_acc, static_cast<long long>(rows), Hq, N, 0, st);
+  if (e == cudaSuccess) e = launch_bwd_score(dtype, d, tk, tv, tq, tdo, tdq, a, N, B, st);
+  if (e == cudaSuccess) e = launch_dq_convert(dtype, dq_acc, dq, static_cast<long long>(rows) * d, scale, st);
+  return launch_status(e);
+}

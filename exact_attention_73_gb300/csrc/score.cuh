@@ -1,0 +1,97 @@
+// Score changes shared by the forward and backward kernels (their kScore
+// instances): a tanh cap, a bias that falls with the distance, and row masks.
+//
+//   x = scale q.k;  cap > 0: x <- cap tanh(x / cap);  x <- x - slope_h |i - j|
+//   row i sees keys lo_i <= j < hi_i, inside the window
+//
+// Everything is in log2 units from the accumulated q.k (s) on. tanh costs two
+// MUFU operations when taken from exp2 and a reciprocal, next to the one exp2
+// a score needs anyway; the MUFU is the unit these kernels have least of. So
+// tanh(w) is w times an even polynomial in w (minimax in relative error,
+// fitted by the Remez exchange): degree 7 for |w| <= 1/2 (5.5e-7), degree 13
+// for |w| <= 1 (5e-8), and 1 - 2 / (1 + exp2(2 w log2 e)) beyond. Which one a
+// warp takes follows from the largest |s| it holds.
+#pragma once
+#include <cmath>
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace attn {
+
+// A score's sub-tile facts, per 64 rows: the union and the intersection of
+// the rows' visible keys. Row i's own are ranges[i] cut by the window.
+struct ScoreArgs {
+  const int2* ranges;       // [B, N] visible keys [x, y) of each row, or null
+  const int4* bounds;       // [B, ntile] per 64 rows: lowest lo, highest hi (of rows that see a key), highest lo, lowest hi
+  const int2* key_tiles;    // backward: [B, ceil(N / 128)] 64-row tiles [x, y) that see a key of the 128
+  int ntile;                // ceil(N / 64)
+  const float* slopes;      // [Hq] or null
+  float sl2;                // scale * log2(e)
+  float cap_log2;           // cap * log2(e), 0: no cap
+  float inv_cap2;           // 1 / cap_log2
+  float w_of_s;             // scale / cap: the tanh's argument is s times this
+  float s_small;            // |s| up to which the degree 7 polynomial is used
+  float k[4];               // its coefficients in s^2, times scale * log2(e)
+};
+
+constexpr float kTanhSmall = 0.5f;
+constexpr float kTanh7[4] = {0.999999456f, -0.333263179f, 0.131902966f, -0.0444022261f};
+
+// Host: the cap's factors. The degree 7 polynomial is evaluated in s^2 with
+// scaled coefficients; where those would leave FP32's comfortable range
+// (scale / cap beyond 1e-6 .. 1e4) it is not used.
+inline void set_cap(ScoreArgs& a, float scale, float cap) {
+  const float log2e = 1.4426950408889634f;
+  a.sl2 = scale * log2e;
+  a.cap_log2 = cap * log2e;
+  a.inv_cap2 = cap > 0.f ? 1.f / a.cap_log2 : 0.f;
+  a.w_of_s = cap > 0.f ? scale / cap : 0.f;
+  const double w = std::fabs(static_cast<double>(a.w_of_s));
+  const bool ok = w >= 1e-6 && w <= 1e4;
+  a.s_small = ok ? static_cast<float>(kTanhSmall / w) : -1.f;
+  double f = static_cast<double>(scale) * log2e;
+  for (int i = 0; i < 4; ++i) {
+    a.k[i] = ok ? static_cast<float>(kTanh7[i] * f) : 0.f;
+    f *= w * w;
+  }
+}
+
+// s -> cap_log2 tanh(s w_of_s) for a pair of scores with |w| <= 1 ...
+__device__ __forceinline__ float2 cap_pair(float2 s, float w_of_s, float cap_log2) {
+  constexpr float c[7] = {0.99999995f,   -0.333328392f,   0.133252041f,   -0.0534570296f,
+                          0.0202899804f, -0.00620337911f, 0.00104102264f};   // degree 13
+  const float2 w = fmul2(s, make_float2(w_of_s, w_of_s));
+  const float2 z = fmul2(w, w);
+  float2 q = make_float2(c[6], c[6]);
+#pragma unroll
+  for (int i = 5; i >= 0; --i) q = ffma2(q, z, make_float2(c[i], c[i]));
+  return fmul2(fmul2(q, w), make_float2(cap_log2, cap_log2));
+}
+// ... and for any s
+__device__ __forceinline__ float cap_any(float s, float w_of_s, float cap_log2) {
+  const float e = ex2(s * (w_of_s * 2.8853900817779268f));   // exp(2 w)
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return fmaf(-2.f * cap_log2, r, cap_log2);
+}
+// degree 7, in s^2: s -> factor q with s q = cap_log2 tanh(s w_of_s)
+__device__ __forceinline__ float2 cap_small_factor(float2 s, const ScoreArgs& a) {
+  const float2 t = fmul2(s, s);
+  float2 q = ffma2(t, make_float2(a.k[3], a.k[3]), make_float2(a.k[2], a.k[2]));
+  q = ffma2(t, q, make_float2(a.k[1], a.k[1]));
+  return ffma2(t, q, make_float2(a.k[0], a.k[0]));
+}
+
+// Visible keys of row i (in [0, N)): the row's range cut by the window.
+__device__ __forceinline__ int2 score_row(const int2* ranges, long long at, int i, int N, int left, int right) {
+  int2 r = ranges ? __ldg(ranges + at) : make_int2(0, N);
+  r.x = max(r.x, 0);
+  r.y = min(r.y, N);
+  if (left >= 0) r.x = max(r.x, i - left);
+  if (right >= 0) r.y = min(r.y, i + right + 1);
+  if (r.x >= r.y) r = make_int2(N, 0);   // sees nothing
+  return r;
+}
+
+}  // namespace attn

@@ -286,6 +286,60 @@ ATTN_API attn_status attn_rope_tables(float* rope_cos, float* rope_sin, const do
                                       void* stream);
 
 /*
+ * The visible keys of every row for documents, prefixes and padding:
+ * row_ranges int32 [B,N,2], row i of sequence b sees keys row_ranges[b,i,0]
+ * <= j < row_ranges[b,i,1]. doc_ids int32 [B,N] (NULL: one document): a
+ * document is a maximal run of equal ids and a row sees its own document
+ * only; a negative id is padding, which sees and is seen by nothing.
+ * prefix_lens int32 [B] (NULL: none), with causal: keys at positions below
+ * prefix_lens[b] are seen by every row of their document, later ones by the
+ * rows at or behind them. causal = 0: rows see their whole document. N <= 2^24.
+ */
+ATTN_API attn_status attn_mask_rows(const int* doc_ids, const int* prefix_lens, int* row_ranges, int B, int N,
+                                    int causal, void* stream);
+
+/* Bytes of workspace attn_fwd_score needs when row_ranges is given: 16 bytes
+ * per 64 rows and 8 per 128, rounded up to 256. */
+ATTN_API size_t attn_score_workspace_size(int B, int N);
+
+/*
+ * Forward, dense, with modified scores (3.1 with x in the place of S):
+ *   x_ij = scale q_i.k_j;  score_cap > 0: x_ij = score_cap tanh(x_ij / score_cap);
+ *   slopes (float32 [Hq] on the device, constants; or NULL): x_ij -= slopes[h] |i - j|;
+ *   row i sees key j iff i - window_left <= j <= i + window_right (-1: no
+ *   bound) and, with row_ranges (int32 [B,N,2], attn_mask_rows' or the
+ *   caller's own, any ranges; NULL: none), row_ranges[b,i,0] <= j < row_ranges[b,i,1];
+ *   O = softmax(x) V over the visible keys, LSE = log sum exp(x).
+ * A row that sees nothing gets O = 0 and LSE = -inf. Operands and layouts as
+ * attn_fwd; every element finite, masked ones too (a masked weight is an
+ * exact zero, and zero times infinity is not). KV tiles that no row of a
+ * query tile sees are skipped. The cap's tanh is exact to 6e-7 of the score.
+ * workspace (attn_score_workspace_size bytes) is needed with row_ranges only.
+ * score_cap negative, infinite or NaN, scale not positive and finite, N >
+ * 2^24: ATTN_ERR_SHAPE.
+ */
+ATTN_API attn_status attn_fwd_score(const void* q, const void* k, const void* v, void* o, float* lse,
+                                    const int* row_ranges, const float* slopes, void* workspace, size_t ws_bytes,
+                                    int B, int Hq, int Hkv, int N, int d, float scale, float score_cap,
+                                    int window_left, int window_right, attn_dtype dtype, void* stream);
+
+/* Bytes of workspace attn_bwd_score needs: attn_bwd_workspace_size plus
+ * attn_score_workspace_size. */
+ATTN_API size_t attn_bwd_score_workspace_size(int B, int Hq, int Hkv, int N, int d);
+
+/*
+ * Backward of attn_fwd_score with the same row_ranges, slopes, score_cap and
+ * window (o and lse from it): as attn_bwd with dS = P o (dP - D) o (1 -
+ * tanh^2(x / score_cap)). Rows that see nothing get dq = 0, keys that nobody
+ * sees dk = dv = 0. No gradient of slopes.
+ */
+ATTN_API attn_status attn_bwd_score(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                                    const void* dout, void* dq, void* dk, void* dv, const int* row_ranges,
+                                    const float* slopes, void* workspace, size_t ws_bytes, int B, int Hq, int Hkv,
+                                    int N, int d, float scale, float score_cap, int window_left, int window_right,
+                                    attn_dtype dtype, void* stream);
+
+/*
  * Append new rows to a block-quantised KV cache (the operand that
  * attn_decode_fp8 and attn_decode_cache_fp8 read), optionally rotating the
  * keys first. k, v: new rows [B,Hkv,n_new,d] of `dtype` (BF16/FP16) with HOST

@@ -63,6 +63,34 @@ def test_cache_refusals(lib):
     assert L.attn_decode_cache_fp8_splits(1, 3, 2, 4) == 0 and L.attn_decode_cache_fp8_splits(1, 4, 2, 0) == 0
 
 
+def test_score_refusals(lib):
+    assert lib.attn_mask_rows(P(), None, None, 1, 8, 1, None) == 1
+    assert lib.attn_mask_rows(P(8), None, P(), 1, 8, 1, None) == 2 and lib.attn_mask_rows(None, P(8), P(), 1, 8, 1, None) == 2
+    for b, n in ((0, 8), (65536, 8), (1, 0), (1, 2 ** 24 + 1)):
+        assert lib.attn_mask_rows(P(), None, P(), b, n, 1, None) == 3
+    w = L.attn_score_workspace_size(2, 300)
+    assert w == 256 and L.attn_score_workspace_size(2, 8192) == 2 * (128 * 16 + 64 * 8) and L.attn_score_workspace_size(0, 8) == 0
+
+    def fwd(q=P(), lse=P(), ranges=None, slopes=None, ws=P(), wb=w, B=2, Hq=4, Hkv=2, N=300, d=64, scale=0.1, cap=0.0, left=-1,
+            right=-1, dt=0):
+        return lib.attn_fwd_score(q, P(), P(), P(), lse, ranges, slopes, ws, wb, B, Hq, Hkv, N, d, scale, cap, left, right, dt, None)
+    assert fwd(q=None) == 1 and fwd(ranges=P(), ws=None) == 1
+    assert fwd(lse=P(20)) == 2 and fwd(ranges=P(8)) == 2 and fwd(slopes=P(4)) == 2
+    assert fwd(B=0) == 3 and fwd(N=0) == 3 and fwd(N=2 ** 24 + 1) == 3 and fwd(left=-2) == 3 and fwd(right=-7) == 3
+    assert fwd(cap=-0.5) == 3 and fwd(cap=math.nan) == 3 and fwd(cap=math.inf) == 3 and fwd(scale=math.nan) == 3
+    assert fwd(scale=0.0) == 3 and fwd(scale=-0.1) == 3
+    assert fwd(d=96) == 4 and fwd(Hkv=3) == 5 and fwd(dt=2) == 6 and fwd(ranges=P(), wb=w - 1) == 7
+    wb_ = L.attn_bwd_score_workspace_size(2, 4, 2, 300, 64)
+    assert wb_ == L.attn_bwd_workspace_size(2, 4, 2, 300, 64) + w and L.attn_bwd_score_workspace_size(0, 4, 2, 300, 64) == 0
+
+    def bwd(do=P(), ranges=None, ws=P(), wb=wb_, B=2, Hq=4, Hkv=2, N=300, d=64, scale=0.1, cap=0.0, left=-1, right=-1, dt=0):
+        return lib.attn_bwd_score(P(), P(), P(), P(), P(), do, P(), P(), P(), ranges, None, ws, wb, B, Hq, Hkv, N, d, scale, cap, left,
+                                  right, dt, None)
+    assert bwd(do=None) == 1 and bwd(ws=None) == 1 and bwd(ranges=P(8)) == 2
+    assert bwd(N=0) == 3 and bwd(left=-2) == 3 and bwd(cap=-1.0) == 3 and bwd(scale=math.inf) == 3
+    assert bwd(d=32) == 4 and bwd(Hkv=3) == 5 and bwd(dt=2) == 6 and bwd(wb=wb_ - 1) == 7
+
+
 class _Lib:
     def __init__(self):
         self.calls = []
@@ -141,6 +169,30 @@ def test_binding_checks_caches(fake):
         L.attn_decode_cache_fp8(q, *dense, lens.long(), o, lse, ws, 1, stream=STREAM)
     with pytest.raises(TypeError):
         L.attn_decode_cache_fp8(q, *dense, lens, o.half(), lse, ws, 1, stream=STREAM)
+    assert fake.calls == []
+
+
+def test_binding_checks_score_calls(fake):
+    q, kv, lse = z(2, 4, 70, 64), z(2, 2, 70, 64), z(2, 4, 70, dtype=F32)
+    rr, sl, ws = z(2, 70, 2, dtype=I32), z(4, dtype=F32), z(4096, dtype=U8)
+    L.attn_mask_rows(rr, doc_ids=z(2, 70, dtype=I32), prefix_lens=z(2, dtype=I32), stream=STREAM)
+    L.attn_fwd_score(q, kv, kv, q, lse, stream=STREAM)
+    L.attn_fwd_score(q, kv, kv, q, lse, workspace=ws, row_ranges=rr, slopes=sl, score_cap=30.0, window=(5, 0), stream=STREAM)
+    L.attn_bwd_score(q, kv, kv, q, lse, q, q, kv, kv, ws, row_ranges=rr, slopes=sl, score_cap=30.0, stream=STREAM)
+    assert [n for n, _ in fake.calls] == ["attn_mask_rows", "attn_fwd_score", "attn_fwd_score", "attn_bwd_score"]
+    assert fake.calls[1][1][7:9] == (None, 0) and fake.calls[2][1][8] == 4096
+    fake.calls.clear()
+    for call in (lambda: L.attn_mask_rows(rr, doc_ids=z(2, 69, dtype=I32), stream=STREAM),
+                 lambda: L.attn_mask_rows(z(2, 70, 3, dtype=I32), stream=STREAM),
+                 lambda: L.attn_mask_rows(rr, prefix_lens=z(3, dtype=I32), stream=STREAM),
+                 lambda: L.attn_fwd_score(q, kv, kv, q, lse, workspace=ws, row_ranges=rr[:1], stream=STREAM),
+                 lambda: L.attn_fwd_score(q, kv, kv, q, lse, slopes=sl[:2], stream=STREAM),
+                 lambda: L.attn_fwd_score(q, kv, kv[:, :, :9], q, lse, stream=STREAM),
+                 lambda: L.attn_bwd_score(q, kv, kv, q, lse, q, q, kv[:1], kv, ws, stream=STREAM)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        L.attn_mask_rows(rr.long(), stream=STREAM)
     assert fake.calls == []
 
 
