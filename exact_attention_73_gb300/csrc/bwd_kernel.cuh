@@ -190,13 +190,32 @@ __device__ __forceinline__ void split_add(uint32_t (&v)[32], const float* part1,
   }
 }
 
+// Bits n and up of a word (all of them for n <= 0, none for n >= 32).
+__device__ __forceinline__ uint32_t bits_from(int n) {
+  return n >= 32 ? 0u : 0xffffffffu << max(n, 0);
+}
+// 32 x 32 bits across a warp: bit e of lane k's result is bit k of lane e's word.
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t x, int lane) {
+  constexpr uint32_t mask[5] = {0x0000ffffu, 0x00ff00ffu, 0x0f0f0f0fu, 0x33333333u, 0x55555555u};
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    const int h = 16 >> i;
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, h);
+    x = (lane & h) ? ((x & ~mask[i]) | ((y >> h) & mask[i])) : ((x & mask[i]) | ((y << h) & ~mask[i]));
+  }
+  return x;
+}
+
 // kDQ = false: dK and dV only (the deterministic backward computes dQ in a
 // separate query-stationary kernel); the dQ^T product, its drain and the
 // reduce-adds are left out.
 // kScore: scores may be capped and biased and rows masked by ranges
 // (score.cuh). dS takes the cap's derivative, 1 - tanh^2 = 1 - (x / cap)^2,
-// from the capped score itself.
-template <int DT, int D, bool kDQ = true, bool kSplit = false, bool kPersist = false, bool kScore = false>
+// from the capped score itself. Row masks: lane e of a warp holds query e's
+// visible keys as a bit for each of the warp's 32 keys; if any bit is
+// missing the 32 x 32 bits are transposed across the warp, so that each lane
+// has its own key's bit for every query.
+template <int DT, int D, bool kDQ = true, bool kSplit = false, bool kPersist = false, int kScore = 0>
 __global__ void __launch_bounds__(512, 1)
 bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
            const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
@@ -257,6 +276,13 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     bx = static_cast<int>(blockIdx.x) % a.tiles_x;
     by = static_cast<int>(blockIdx.x) / a.tiles_x % a.Hkv;
     bz = static_cast<int>(blockIdx.x) / a.tiles_x / a.Hkv;
+  } else if constexpr ((kScore & kScoreRanges) != 0) {
+    const int lin = bx + static_cast<int>(gridDim.x) * (by + static_cast<int>(gridDim.y) * bz);
+    int pos;
+    heavy_first_map(16, lin, static_cast<int>(gridDim.x * gridDim.z), static_cast<int>(gridDim.y), 1, pos, by, bz);
+    const int2 u = __ldg(a.sc.order + pos / C::DSPLIT);
+    bx = u.x * C::DSPLIT + pos % C::DSPLIT;
+    bz = u.y;
   } else if (a.causal) {
     // with causal masking key tile 0 has the most work: heavy tiles start
     // first. Packed sequences run in blocks of 64 key tiles per (sequence,
@@ -287,12 +313,10 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     const int qhi = a.win_left < 0 ? L - 1 : min(L - 1, klast + a.win_left);
     i0 = qlo / C::BR;
     per_head = qhi / C::BR + 1 - i0;
-    if constexpr (kScore) {
-      if (a.sc.ranges) {
-        const int2 t = __ldg(a.sc.key_tiles + static_cast<long long>(b) * ((a.N + C::BC - 1) / C::BC) + j);
-        i0 = t.x;
-        per_head = t.y - t.x;
-      }
+    if constexpr ((kScore & kScoreRanges) != 0) {
+      const int2 t = __ldg(a.sc.key_tiles + static_cast<long long>(b) * ((a.N + C::BC - 1) / C::BC) + j);
+      i0 = t.x;
+      per_head = t.y - t.x;
     }
     // this CTA's part of the walk over (query head, query tile): iterations
     // it_base .. it_base + niter - 1 of the group * per_head
@@ -663,11 +687,19 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
         const uint32_t xb = tbase + lane_off + 128u * (g & 1);
         uint8_t* ds_row = sDS + (C::NDS > 1 ? (g & 1) * C::DS_B : 0) + r * 128;
         const int st = g % C::NQ;
-        int4 bnd = make_int4(0, 0, 0, 0);   // visible keys of the tile's rows: intersection in .z, .w
+        constexpr bool kCap = (kScore & kScoreCap) != 0, kBias = (kScore & kScoreBias) != 0,
+                       kRanges = (kScore & kScoreRanges) != 0;
+        // fetched before the waits, which cover the latency
         float slope2 = 0.f;
-        if constexpr (kScore) {   // fetched before the waits, which cover the latency
-          if (a.sc.ranges) bnd = __ldg(a.sc.bounds + static_cast<long long>(b) * a.sc.ntile + q_tile(it));
-          if (a.sc.slopes) slope2 = __ldg(a.sc.slopes + q_head(it)) * kLog2e;
+        if constexpr (kBias) slope2 = __ldg(a.sc.slopes + q_head(it)) * kLog2e;
+        uint32_t seen = 0;   // lane e: which of the warp's keys query e of this group's 32 sees
+        if constexpr (kRanges) {
+          const int q = q_tile(it) * C::BR + 32 * half + lane;
+          if (q < L) {
+            const int2 v = score_row(a.sc.ranges, static_cast<long long>(b) * L + q, q, L, a.win_left, a.win_right);
+            const int k0 = j * C::BC + quarter * 32;
+            seen = bits_from(v.x - k0) & ~bits_from(v.y - k0);
+          }
         }
         // LSE and D of this stage (written by the load warp before it arrived
         // on q_full[st]) go to registers first: these shared-memory reads then
@@ -701,22 +733,21 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
         if (!ok) break;
         const int q0 = q_tile(it) * C::BR + 32 * half;
         // this key against queries q0 .. q0 + 31: outside the sequence or the window?
-        bool edge = kPersist ? !kvalid
-                                   : !kvalid || (a.win_right >= 0 && kloc > q0 + a.win_right) ||
-                                         (a.win_left >= 0 && kloc < q0 + 31 - a.win_left);
-        if constexpr (kScore) {
-          if (a.sc.ranges) edge = !kvalid || kloc < bnd.z || kloc >= bnd.w;
-          if (a.sc.cap_log2 > 0.f) {   // capped scores in place of the raw ones
-            const float big = rowmax_abs(sv);
-            if (!warp_any(!(big <= a.sc.s_small))) {
-  #pragma unroll
-              for (int c = 0; c < 32; c += 2) {
-                const float2 s2 = make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-                const float2 y = fmul2(s2, cap_small_factor(s2, a.sc));
-                sv[c] = __float_as_uint(y.x);
-                sv[c + 1] = __float_as_uint(y.y);
-              }
-            } else if (!warp_any(!(big * fabsf(a.sc.w_of_s) <= 1.f))) {
+        bool edge;
+        if constexpr (kRanges) {
+          edge = warp_any(seen != 0xffffffffu);
+          if (edge) seen = transpose_bits(seen, lane);   // now: which of the queries see this lane's key
+        } else {
+          edge = kPersist ? !kvalid
+                          : !kvalid || (a.win_right >= 0 && kloc > q0 + a.win_right) ||
+                                (a.win_left >= 0 && kloc < q0 + 31 - a.win_left);
+        }
+        bool raw = true;   // capped: sv holds raw scores, small enough for the polynomial in the loop
+        if constexpr (kCap) {
+          const float big = rowmax_abs(sv);
+          raw = !warp_any(!(big <= a.sc.s_small));
+          if (!raw) {
+            if (!warp_any(!(big * fabsf(a.sc.w_of_s) <= 1.f))) {
   #pragma unroll
               for (int c = 0; c < 32; c += 2) {
                 const float2 y = cap_pair(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), a.sc.w_of_s,
@@ -731,27 +762,38 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
             }
           }
         }
+        // the bias joins -LSE: where every query lies at or behind every key
+        // it is linear, -slope (q - key), from one value per lane
+        const bool behind = q0 >= j * C::BC + quarter * 32 + 31;
+        const float from = static_cast<float>(q0 - kloc);
         uint32_t pp[16], dd[16];
-        // kCap: sv holds capped log2 scores, and dS takes the cap's derivative
-        auto weights = [&](auto cap) {
-          constexpr bool kCap = decltype(cap)::value;
+        auto weights = [&](auto raw_scores) {
+          constexpr bool kRaw = decltype(raw_scores)::value;
   #pragma unroll
         for (int e4 = 0; e4 < 8; ++e4) {
           float4 l4 = l4r[e4];
           const float4 d4 = d4r[e4];
-          if constexpr (kScore) {
-            if (a.sc.slopes) {   // the bias joins -LSE
-              const float from = static_cast<float>(q0 + 4 * e4 - kloc);
-              l4.x = fmaf(-slope2, fabsf(from), l4.x);
-              l4.y = fmaf(-slope2, fabsf(from + 1.f), l4.y);
-              l4.z = fmaf(-slope2, fabsf(from + 2.f), l4.z);
-              l4.w = fmaf(-slope2, fabsf(from + 3.f), l4.w);
+          if constexpr (kBias) {
+            if (behind) {
+              const float2 f = make_float2(from, from), n = make_float2(-slope2, -slope2);
+              const float2 u = ffma2(n, fadd2(f, make_float2(4.f * e4, 4.f * e4 + 1.f)), make_float2(l4.x, l4.y));
+              const float2 w = ffma2(n, fadd2(f, make_float2(4.f * e4 + 2.f, 4.f * e4 + 3.f)), make_float2(l4.z, l4.w));
+              l4 = make_float4(u.x, u.y, w.x, w.y);
+            } else {
+              l4.x = fmaf(-slope2, fabsf(from + 4.f * e4), l4.x);
+              l4.y = fmaf(-slope2, fabsf(from + (4.f * e4 + 1.f)), l4.y);
+              l4.z = fmaf(-slope2, fabsf(from + (4.f * e4 + 2.f)), l4.z);
+              l4.w = fmaf(-slope2, fabsf(from + (4.f * e4 + 3.f)), l4.w);
             }
           }
-          const float2 s01 = make_float2(__uint_as_float(sv[4 * e4]), __uint_as_float(sv[4 * e4 + 1]));
-          const float2 s23 = make_float2(__uint_as_float(sv[4 * e4 + 2]), __uint_as_float(sv[4 * e4 + 3]));
+          float2 s01 = make_float2(__uint_as_float(sv[4 * e4]), __uint_as_float(sv[4 * e4 + 1]));
+          float2 s23 = make_float2(__uint_as_float(sv[4 * e4 + 2]), __uint_as_float(sv[4 * e4 + 3]));
           float2 x01, x23;
           if constexpr (kCap) {
+            if constexpr (kRaw) {
+              s01 = fmul2(s01, cap_small_factor(s01, a.sc));
+              s23 = fmul2(s23, cap_small_factor(s23, a.sc));
+            }
             x01 = fadd2(s01, make_float2(l4.x, l4.y));
             x23 = fadd2(s23, make_float2(l4.z, l4.w));
           } else {
@@ -763,14 +805,9 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
   #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const int q = q0 + 4 * e4 + u;
-              if constexpr (kScore) {
-                if (a.sc.ranges) {
-                  const int2 r = q < L ? score_row(a.sc.ranges, static_cast<long long>(b) * L + q, q, L, a.win_left,
-                                                   a.win_right)
-                                       : make_int2(L, 0);
-                  if (kloc < r.x || kloc >= r.y) p[u] = 0.f;
-                  continue;
-                }
+              if constexpr (kRanges) {
+                if (!(seen >> (4 * e4 + u) & 1u)) p[u] = 0.f;
+                continue;
               }
               if (!kvalid || (a.win_right >= 0 && kloc > q + a.win_right) || (a.win_left >= 0 && kloc < q - a.win_left))
                 p[u] = 0.f;
@@ -801,11 +838,11 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
           }
         }
         };
-        if constexpr (kScore) {
-          if (a.sc.cap_log2 > 0.f) weights(std::true_type{});
+        if constexpr (kCap) {
+          if (raw) weights(std::true_type{});
           else weights(std::false_type{});
         } else {
-          weights(std::false_type{});
+          weights(std::true_type{});
         }
         tmem_st16(xb + C::col_p(2 * half), pp);
         tmem_st16(xb + C::col_ds(2 * half), dd);

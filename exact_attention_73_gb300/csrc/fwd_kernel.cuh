@@ -27,14 +27,12 @@
 #pragma once
 #include <cmath>
 #include <cstdint>
-#include <type_traits>
-
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "ptx.cuh"
-#include "score.cuh"
+#include "score_softmax.cuh"
 
 namespace attn {
 
@@ -158,10 +156,16 @@ __device__ __forceinline__ int fwd_unit_of(const FwdArgs& a, int k) {
 
 // Decode unit `lin`; false when it holds no query row (a packed sequence
 // shorter than the longest one).
-template <int QT, bool kScore = false>
+template <int QT, int kScore = 0>
 __device__ __forceinline__ bool fwd_unit(const FwdArgs& a, int lin, FwdUnit& w) {
   int bx, by, bz;
-  if (a.causal) {
+  if constexpr ((kScore & kScoreRanges) != 0) {
+    int pos;
+    heavy_first_map(8, lin, a.ux * a.uz, a.uy, 1, pos, by, bz);
+    const int2 u = __ldg(a.sc.order + pos);
+    bx = u.x;
+    bz = u.y;
+  } else if (a.causal) {
     // the last query tiles have the most work: those of every (head, batch)
     // come first
     heavy_first_map(8, lin, a.ux, a.uy, a.uz, bx, by, bz);
@@ -182,26 +186,24 @@ __device__ __forceinline__ bool fwd_unit(const FwdArgs& a, int lin, FwdUnit& w) 
   }
   w.nqt = (w.L + 127) >> 7;
   // causal: the units with the most KV tiles first
-  const int cblk = a.causal ? a.ux - 1 - bx : bx;
+  const int cblk = a.causal && !(kScore & kScoreRanges) ? a.ux - 1 - bx : bx;
   w.qt0 = cblk * QT;
   if (w.qt0 >= w.nqt) return false;
   // KV tiles that hold a key visible to some query row of the unit
   const int r0 = w.qt0 * 128, r1 = min((w.qt0 + QT) * 128, w.L);
   int klo = a.win_left < 0 ? 0 : max(0, r0 - a.win_left);
   int khi = a.win_right < 0 ? w.L : min(w.L, r1 + a.win_right);   // exclusive
-  if constexpr (kScore) {
-    if (a.sc.ranges) {   // the union over the unit's 64-row tiles; rows that see nothing get one masked tile
-      klo = w.L;
-      khi = 0;
-      for (int i = w.qt0 * 2; i < min((w.qt0 + QT) * 2, a.sc.ntile); ++i) {
-        const int4 t = __ldg(a.sc.bounds + static_cast<long long>(w.b) * a.sc.ntile + i);
-        klo = min(klo, t.x);
-        khi = max(khi, t.y);
-      }
-      if (klo >= khi) {
-        klo = 0;
-        khi = 1;
-      }
+  if constexpr ((kScore & kScoreRanges) != 0) {   // the union over the unit's 64-row tiles
+    klo = w.L;
+    khi = 0;
+    for (int i = w.qt0 * 2; i < min((w.qt0 + QT) * 2, a.sc.ntile); ++i) {
+      const int2 t = __ldg(a.sc.bounds + static_cast<long long>(w.b) * a.sc.ntile + i);
+      klo = min(klo, t.x);
+      khi = max(khi, t.y);
+    }
+    if (klo >= khi) {   // rows that see nothing get one masked tile
+      klo = 0;
+      khi = 1;
     }
   }
   w.kv0 = klo >> 7;
@@ -214,8 +216,11 @@ __device__ __forceinline__ bool fwd_unit(const FwdArgs& a, int lin, FwdUnit& w) 
 // kPersist: the grid is smaller than the unit count and each CTA walks its
 // units; otherwise every CTA takes one unit and the unit loops below run
 // once (known at compile time, so their bookkeeping folds away).
-// kScore: scores may be capped and biased and rows masked by ranges (score.cuh).
-template <int DT, int D, int QT, bool kPersist, bool kScore = false>
+// kScore: scores capped or biased, rows masked by ranges (score.cuh).
+//
+// Biased scores walk the keys from the last to the first, so that the running
+// max starts near the row's own position, where the bias is least.
+template <int DT, int D, int QT, bool kPersist, int kScore = 0>
 __global__ void __launch_bounds__(FwdCfg<DT, D, QT>::NTHREADS, 1)
 fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
            const __grid_constant__ CUtensorMap tmV, const FwdArgs a) {
@@ -305,7 +310,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
           int jt;
           kv_item(QT, it, w.nkv, is_v, jt);
           const CUtensorMap* m = is_v ? &tmV : &tmK;
-          const int row = w.seq0 + (w.kv0 + jt) * 128;
+          const int row = w.seq0 + (w.kv0 + ((kScore & kScoreBias) ? w.nkv - 1 - jt : jt)) * 128;
           for (int c = 0; c < C::NBOX; ++c) {
             uint8_t* dst = sKV + slot * C::TILE_B + c * C::BOXT_B;
             if (packed) tma_load_4d(dst, m, &kv_full[slot], c * C::BOX_E, w.hkv, row, 0);
@@ -477,11 +482,12 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       float l = 0.f;           // running sum of exp2(x - m)
       int2 vis = make_int2(0, L);   // kScore: this row's visible keys
       float slope2 = 0.f;
-      if constexpr (kScore) {
+      if constexpr (kScore != 0) {
         if (qrow < L)
-          vis = score_row(a.sc.ranges, static_cast<long long>(w.b) * L + qrow, qrow, L, a.win_left, a.win_right);
-        if (a.sc.slopes) slope2 = __ldg(a.sc.slopes + w.h) * 1.4426950408889634f;
+          vis = score_row((kScore & kScoreRanges) ? a.sc.ranges : nullptr, static_cast<long long>(w.b) * L + qrow, qrow,
+                          L, a.win_left, a.win_right);
       }
+      if constexpr ((kScore & kScoreBias) != 0) slope2 = __ldg(a.sc.slopes + w.h) * 1.4426950408889634f;
       int f_run = -1000;       // FP8: running max exponent of the V factors
       float q_fac = 1.f;
       long long vs_base = 0;
@@ -511,119 +517,82 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[sb], sphase, a.status));
         if (!ok) break;
         tc_fence_after();
-        uint32_t sr[128];
+        constexpr bool kCap = (kScore & kScoreCap) != 0, kBias = (kScore & kScoreBias) != 0;
+        constexpr bool kChanged = kCap || kBias;
+        uint32_t sr[kChanged ? 1 : 128];
+        if constexpr (!kChanged) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
-        tmem_wait_ld();
+          for (int c = 0; c < 4; ++c)
+            tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) reg_fence(*reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
-        const int kb = (kv0 + j) * 128;
+          for (int c = 0; c < 4; ++c) reg_fence(*reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
+        }
+        const int kb = (kv0 + ((kScore & kScoreBias) ? nkv - 1 - j : j)) * 128;
         // mask keys past the sequence and outside the window [qrow - left, qrow + right]
         bool edge;
-        if constexpr (kScore) {
+        if constexpr (kScore != 0) {
           edge = warp_any(vis.x > kb || vis.y < kb + 128);
         } else {
           edge = kb + 128 > L || (a.win_right >= 0 && kb + 127 > qtile * 128 + a.win_right) ||
                  (a.win_left >= 0 && kb < qtile * 128 + 127 - a.win_left);
         }
-        // kScore: a capped tile with small scores, no bias and no mask keeps
-        // its raw scores; tanh is folded into the exponent below. Otherwise
-        // the scores become their final log2 values here.
-        bool fused = false, final_scores = false;
-        if constexpr (kScore) {
-          if (a.sc.cap_log2 > 0.f || a.sc.slopes) {
-            float big = 0.f;
-            if (a.sc.cap_log2 > 0.f) big = rowmax_abs(sr);
-            fused = a.sc.cap_log2 > 0.f && !a.sc.slopes && !edge && !warp_any(!(big <= a.sc.s_small));
-            if (!fused) {
-              final_scores = true;
-              if (a.sc.cap_log2 > 0.f) {
-                if (!warp_any(!(big * fabsf(a.sc.w_of_s) <= 1.f))) {
-#pragma unroll
-                  for (int c = 0; c < 128; c += 2) {
-                    const float2 y = cap_pair(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
-                                              a.sc.w_of_s, a.sc.cap_log2);
-                    sr[c] = __float_as_uint(y.x);
-                    sr[c + 1] = __float_as_uint(y.y);
-                  }
-                } else {
-#pragma unroll
-                  for (int c = 0; c < 128; ++c)
-                    sr[c] = __float_as_uint(cap_any(__uint_as_float(sr[c]), a.sc.w_of_s, a.sc.cap_log2));
-                }
-              } else {
-                const float2 f = make_float2(a.sc.sl2, a.sc.sl2);
-#pragma unroll
-                for (int c = 0; c < 128; c += 2) {
-                  const float2 y = fmul2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), f);
-                  sr[c] = __float_as_uint(y.x);
-                  sr[c + 1] = __float_as_uint(y.y);
-                }
-              }
-              if (a.sc.slopes) {
-                const float from = static_cast<float>(kb - qrow);   // key - row of column 0
-#pragma unroll
-                for (int c = 0; c < 128; ++c)
-                  sr[c] = __float_as_uint(fmaf(-slope2, fabsf(from + static_cast<float>(c)), __uint_as_float(sr[c])));
-              }
+        float mx = 0.f;             // largest score of the row (raw unless kChanged)
+        ScoreStep step{};
+        if constexpr (kChanged) {
+          step = score_step<kCap, kBias>(tS, a.sc, m + C::kTau, edge, slope2, kb - qrow, vis.x - kb, vis.y - kb);
+          mx = step.mx;
+        } else {
+          if (edge) {
+            int hi, lo;                                                  // visible: lo <= c < hi
+            if constexpr (kScore != 0) {
+              lo = vis.x - kb;
+              hi = vis.y - kb;
+            } else {
+              hi = L - kb;
+              if (a.win_right >= 0) hi = min(hi, qrow + a.win_right - kb + 1);
+              lo = a.win_left >= 0 ? qrow - a.win_left - kb : 0;
             }
-          }
-        }
-        if (edge) {
-          int hi, lo;                                                  // visible: lo <= c < hi
-          if constexpr (kScore) {
-            lo = vis.x - kb;
-            hi = vis.y - kb;
-          } else {
-            hi = L - kb;
-            if (a.win_right >= 0) hi = min(hi, qrow + a.win_right - kb + 1);
-            lo = a.win_left >= 0 ? qrow - a.win_left - kb : 0;
-          }
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= hi || c < lo) sr[c] = __float_as_uint(-INFINITY);
+            for (int c = 0; c < 128; ++c)
+              if (c >= hi || c < lo) sr[c] = __float_as_uint(-INFINITY);
+          }
+          mx = rowmax(sr);
         }
-        const float mx = rowmax(sr);
         float sl2 = a.scale_log2;
         int f_j = 0, f_new = 0;
+        if constexpr (kChanged) sl2 = 1.f;
         if constexpr (C::kFp8) {
           sl2 *= q_fac * sk_j;
           f_j = pow2_exponent_of(sv_j);
           f_new = max(f_run, f_j);
         }
-        float mxs = mx * sl2;
-        if constexpr (kScore) {
-          if (final_scores) {
-            sl2 = 1.f;
-            mxs = mx;
-          } else if (fused) {   // tanh rises: the largest score is that of the largest raw one
-            mxs = mx * cap_small_factor(make_float2(mx, mx), a.sc).x;
+        if (!kChanged || !step.keep_max) {
+          const float mxs = mx * sl2;
+          const float m_new = (mxs > m + C::kTau) ? mxs : m;
+          float corr = 1.f;
+          if (m_new != m) corr = ex2(m - m_new);   // m = -inf gives 0
+          float corr_o = corr;
+          if constexpr (C::kFp8) {
+            if (f_new != f_run) corr_o *= exp2i(max(f_run - f_new, -126));
           }
-        }
-        const float m_new = (mxs > m + C::kTau) ? mxs : m;
-        float corr = 1.f;
-        if (m_new != m) corr = ex2(m - m_new);   // m = -inf gives 0
-        float corr_o = corr;
-        if constexpr (C::kFp8) {
-          if (f_new != f_run) corr_o *= exp2i(max(f_run - f_new, -126));
-        }
-        l *= corr;
-        m = m_new;
-        if (j > 0 && warp_any(corr_o != 1.f)) {
-          if constexpr (QT == 1) {   // PV(j-1) may still be running with two score buffers
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(o_done, (gj - 1) & 1, a.status)))) break;
-            tc_fence_after();
-          }
+          l *= corr;
+          m = m_new;
+          if (j > 0 && warp_any(corr_o != 1.f)) {
+            if constexpr (QT == 1) {   // PV(j-1) may still be running with two score buffers
+              if (!(ok = __all_sync(0xffffffffu, mbar_wait(o_done, (gj - 1) & 1, a.status)))) break;
+              tc_fence_after();
+            }
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t r[32];
-            tmem_ld32(tO + 32 * c, r);
-            tmem_wait_ld();
-            reg_fence(r);
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t r[32];
+              tmem_ld32(tO + 32 * c, r);
+              tmem_wait_ld();
+              reg_fence(r);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * corr_o);
-            tmem_st32(tO + 32 * c, r);
+              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * corr_o);
+              tmem_st32(tO + 32 * c, r);
+            }
           }
         }
         const float mu = (m == -INFINITY) ? 0.f : m;
@@ -649,31 +618,21 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             }
             tmem_st8(tS + 8 * c, pk);
           }
+        } else if constexpr (kChanged) {
+          score_weights<DT == kBF16, kCap, kBias>(tS, a.sc, step.way, slope2, kb - qrow, bias, acc);
         } else {
-          // kCap: the exponent is s times the degree 7 polynomial in s^2
-          auto weights = [&](auto cap) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t pk[16];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int i = 32 * c + 2 * e;
-                const float2 sp = make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
-                float2 f = sl2v;
-                if constexpr (decltype(cap)::value) f = cap_small_factor(sp, a.sc);
-                float2 x = ffma2(sp, f, biasv);
-                x = make_float2(ex2(x.x), ex2(x.y));
-                acc[e & 3] = fadd2(acc[e & 3], x);
-                pk[e] = (DT == kBF16) ? pack_bf16x2(x.x, x.y) : pack_f16x2(x.x, x.y);
-              }
-              tmem_st16(tS + 16 * c, pk);
+            for (int e = 0; e < 16; ++e) {
+              const int i = 32 * c + 2 * e;
+              float2 x = ffma2(make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), sl2v, biasv);
+              x = make_float2(ex2(x.x), ex2(x.y));
+              acc[e & 3] = fadd2(acc[e & 3], x);
+              pk[e] = (DT == kBF16) ? pack_bf16x2(x.x, x.y) : pack_f16x2(x.x, x.y);
             }
-          };
-          if constexpr (kScore) {
-            if (fused) weights(std::true_type{});
-            else weights(std::false_type{});
-          } else {
-            weights(std::false_type{});
+            tmem_st16(tS + 16 * c, pk);
           }
         }
         const float2 a01 = fadd2(acc[0], acc[1]), a23 = fadd2(acc[2], acc[3]);
@@ -696,7 +655,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       tc_fence_after();
       if (!ok) break;
       float inv = 1.f / l;
-      if constexpr (kScore) {
+      if constexpr (kScore != 0) {
         if (l == 0.f) inv = 0.f;   // the row sees nothing: O = 0, LSE = -inf
       }
       if constexpr (C::kFp8) inv *= exp2i(f_run - C::kPShift);

@@ -20,7 +20,7 @@ inline bool fwd_persistent(int qt, const FwdArgs& a, int rows) {
   return a.win_left >= 0 && a.win_right >= 0 && a.win_left + a.win_right + 256 <= kFwdPersistMaxRows;
 }
 
-template <int DT, int D, int QT, bool kPersist, bool kScore = false>
+template <int DT, int D, int QT, bool kPersist, int kScore = 0>
 cudaError_t launch_fwd_grid(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const FwdArgs& u,
                             long long units, cudaStream_t st) {
   using C = FwdCfg<DT, D, QT>;
@@ -57,17 +57,27 @@ cudaError_t launch_fwd_inst(const CUtensorMap& q, const CUtensorMap& k, const CU
   return launch_fwd_grid<DT, D, QT, false>(q, k, v, u, units, st);
 }
 
-// Score-modified instance (score.cuh): one unit per CTA.
+// Score-modified instances (score.cuh): one unit per CTA. `mode`: kScoreCap,
+// kScoreBias, kScoreRanges together, not 0.
 template <int DT, int D, int QT>
-cudaError_t launch_fwd_score_inst(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const FwdArgs& a,
-                                  int rows, int gy, int gz, cudaStream_t st) {
+cudaError_t launch_fwd_score_inst(int mode, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                                  const FwdArgs& a, int rows, int gy, int gz, cudaStream_t st) {
   FwdArgs u = a;
   u.ux = (rows + 128 * QT - 1) / (128 * QT);
   u.uy = gy;
   u.uz = gz;
   const long long units = static_cast<long long>(u.ux) * gy * gz;
   if (units > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_fwd_grid<DT, D, QT, false, true>(q, k, v, u, units, st);
+  switch (mode) {
+    case 1: return launch_fwd_grid<DT, D, QT, false, 1>(q, k, v, u, units, st);
+    case 2: return launch_fwd_grid<DT, D, QT, false, 2>(q, k, v, u, units, st);
+    case 3: return launch_fwd_grid<DT, D, QT, false, 3>(q, k, v, u, units, st);
+    case 4: return launch_fwd_grid<DT, D, QT, false, 4>(q, k, v, u, units, st);
+    case 5: return launch_fwd_grid<DT, D, QT, false, 5>(q, k, v, u, units, st);
+    case 6: return launch_fwd_grid<DT, D, QT, false, 6>(q, k, v, u, units, st);
+    case 7: return launch_fwd_grid<DT, D, QT, false, 7>(q, k, v, u, units, st);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace attn

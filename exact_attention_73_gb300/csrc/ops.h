@@ -38,10 +38,16 @@ bool accum_map(CUtensorMap* m, const float* base, int d, bool packed, int B, int
 // (the box of its map).
 int bwd_dq_rows(int d);
 int bwd_dq_dims(int d);
-// Score-modified main kernel (BwdArgs::sc set), dense.
-cudaError_t launch_bwd_score(int dt, int d, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
-                             const CUtensorMap& dout, const CUtensorMap& dq_acc, const BwdArgs& a, int N, int nz,
-                             cudaStream_t st);
+// Score-modified main kernels (BwdArgs::sc set; mode: what they change), dense.
+cudaError_t launch_bwd_score_64(int mode, int dt, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
+                                const CUtensorMap& dout, const CUtensorMap& dq_acc, const BwdArgs& a, int N, int nz,
+                                cudaStream_t st);
+cudaError_t launch_bwd_score_128(int mode, int dt, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
+                                 const CUtensorMap& dout, const CUtensorMap& dq_acc, const BwdArgs& a, int N, int nz,
+                                 cudaStream_t st);
+cudaError_t launch_bwd_score_256(int mode, int dt, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
+                                 const CUtensorMap& dout, const CUtensorMap& dq_acc, const BwdArgs& a, int N, int nz,
+                                 cudaStream_t st);
 cudaError_t launch_bwd_dkdv(int dt, int d, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
                             const CUtensorMap& dout, const BwdArgs& a, int max_len, int nz, cudaStream_t st);
 cudaError_t launch_bwd_dq(int dt, int d, const CUtensorMap& q, const CUtensorMap& dout, const CUtensorMap& k,

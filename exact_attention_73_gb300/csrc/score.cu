@@ -8,10 +8,11 @@
 // the neighbouring ids, all threads at a time (a CTA reads at most the run).
 // Four bytes in and eight out per row.
 //
-// Tile facts. Per 64 rows the union and the intersection of the rows' visible
-// keys: the forward takes the union as its KV range, both kernels skip the
-// mask where a tile lies inside the intersection. Per 128 keys the 64-row
-// tiles that see one of them: the backward's walk.
+// Tile facts. Per 64 rows the union of the rows' visible keys: the forward's
+// KV range. Per 128 keys the 64-row tiles that see one of them: the
+// backward's walk. From these the order of the units, most work first (a
+// counting sort): with documents the work of neighbouring tiles differs by
+// their length, and a long one started last would run alone.
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -129,11 +130,11 @@ __global__ void __launch_bounds__(256) mask_rows_kernel(const int* __restrict__ 
 }
 
 // One warp per 64 rows.
-__global__ void __launch_bounds__(256) score_bounds_kernel(const int2* __restrict__ ranges, int4* __restrict__ bounds,
+__global__ void __launch_bounds__(256) score_bounds_kernel(const int2* __restrict__ ranges, int2* __restrict__ bounds,
                                                            int N, int ntile, int left, int right) {
   const int i = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, b = blockIdx.y;
   if (i >= ntile) return;
-  int4 v = make_int4(N, 0, 0, N);
+  int2 v = make_int2(N, 0);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int r = i * 64 + lane + 32 * u;
@@ -141,24 +142,20 @@ __global__ void __launch_bounds__(256) score_bounds_kernel(const int2* __restric
     const int2 s = score_row(ranges, static_cast<long long>(b) * N + r, r, N, left, right);   // (N, 0) if empty
     v.x = min(v.x, s.x);
     v.y = max(v.y, s.y);
-    v.z = max(v.z, s.x);
-    v.w = min(v.w, s.y);
   }
   v.x = __reduce_min_sync(0xffffffffu, v.x);
   v.y = __reduce_max_sync(0xffffffffu, v.y);
-  v.z = __reduce_max_sync(0xffffffffu, v.z);
-  v.w = __reduce_min_sync(0xffffffffu, v.w);
   if (lane == 0) bounds[static_cast<long long>(b) * ntile + i] = v;
 }
 
 // One warp per 128 keys: the first and last 64-row tile with a row that may see one.
-__global__ void __launch_bounds__(256) score_key_tiles_kernel(const int4* __restrict__ bounds, int2* __restrict__ key_tiles,
+__global__ void __launch_bounds__(256) score_key_tiles_kernel(const int2* __restrict__ bounds, int2* __restrict__ key_tiles,
                                                               int ntile, int nkey) {
   const int j = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, b = blockIdx.y;
   if (j >= nkey) return;
   int lo = ntile, hi = 0;
   for (int i = lane; i < ntile; i += 32) {
-    const int4 v = bounds[static_cast<long long>(b) * ntile + i];
+    const int2 v = bounds[static_cast<long long>(b) * ntile + i];
     if (v.x < (j + 1) * 128 && v.y > j * 128) {
       lo = min(lo, i);
       hi = max(hi, i + 1);
@@ -171,6 +168,55 @@ __global__ void __launch_bounds__(256) score_key_tiles_kernel(const int4* __rest
     hi = 1;
   }
   if (lane == 0) key_tiles[static_cast<long long>(b) * nkey + j] = make_int2(lo, hi);
+}
+
+// Counting sort of the units (x, b), x < nx, by their tiles, most first, in
+// kBins levels of work (`most` tiles: the highest). group > 0: unit x unites
+// `group` 64-row tiles of `facts` (the forward's bounds, work in KV tiles);
+// group = 0: facts[b * nx + x] is the unit's walk (the backward's key tiles).
+constexpr int kBins = 1024;
+__global__ void __launch_bounds__(kBins) score_order_kernel(const int2* __restrict__ facts, int2* __restrict__ order,
+                                                            int B, int nx, int group, int ntile, int most) {
+  __shared__ int count[kBins];
+  __shared__ int warp_sum[32];
+  const int t = threadIdx.x, lane = t & 31;
+  count[t] = 0;
+  __syncthreads();
+  const long long units = static_cast<long long>(B) * nx;
+  auto level = [&](long long u) {
+    const int b = static_cast<int>(u / nx), x = static_cast<int>(u % nx);
+    int work;
+    if (group == 0) {
+      const int2 v = facts[u];
+      work = v.y - v.x;
+    } else {
+      int lo = INT_MAX, hi = 0;
+      for (int i = x * group; i < min((x + 1) * group, ntile); ++i) {
+        const int2 v = facts[static_cast<long long>(b) * ntile + i];
+        lo = min(lo, v.x);
+        hi = max(hi, v.y);
+      }
+      work = lo < hi ? ((hi + 127) >> 7) - (lo >> 7) : 1;
+    }
+    return kBins - 1 - static_cast<int>(static_cast<long long>(min(work, most)) * (kBins - 1) / most);
+  };
+  for (long long u = t; u < units; u += kBins) atomicAdd(&count[level(u)], 1);
+  __syncthreads();
+  // exclusive prefix sum over the levels
+  const int n = count[t];
+  int s = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  if (lane == 31) warp_sum[t >> 5] = s;
+  __syncthreads();
+  for (int w = 0; w < (t >> 5); ++w) s += warp_sum[w];
+  count[t] = s - n;
+  __syncthreads();
+  for (long long u = t; u < units; u += kBins)
+    order[atomicAdd(&count[level(u)], 1)] = make_int2(static_cast<int>(u % nx), static_cast<int>(u / nx));
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -187,22 +233,37 @@ attn_status check_score(const int* row_ranges, const float* slopes, float scale,
   return ATTN_OK;
 }
 
+// The workspace's parts: bounds, key tiles and the order of the units (of the
+// forward's 128 or 256 rows, or of the backward's 128 keys).
 cudaError_t prepare_score(ScoreArgs& a, const int* row_ranges, const float* slopes, float scale, float cap, int B,
-                          int N, int left, int right, void* facts, bool keys, cudaStream_t st) {
+                          int N, int left, int right, void* facts, int unit_rows, bool keys, cudaStream_t st) {
   set_cap(a, scale, cap);
   a.slopes = slopes;
   a.ntile = ntiles(N);
   if (!row_ranges) return cudaSuccess;
   a.ranges = reinterpret_cast<const int2*>(row_ranges);
-  int4* bounds = static_cast<int4*>(facts);
+  int2* bounds = static_cast<int2*>(facts);
+  int2* kt = bounds + static_cast<size_t>(B) * a.ntile;
+  int2* order = kt + static_cast<size_t>(B) * nkeys(N);
   a.bounds = bounds;
+  a.key_tiles = kt;
+  a.order = order;
   score_bounds_kernel<<<dim3((a.ntile + 7) / 8, B), 256, 0, st>>>(a.ranges, bounds, N, a.ntile, left, right);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !keys) return e;
-  int2* kt = reinterpret_cast<int2*>(bounds + static_cast<size_t>(B) * a.ntile);
-  a.key_tiles = kt;
-  score_key_tiles_kernel<<<dim3((nkeys(N) + 7) / 8, B), 256, 0, st>>>(bounds, kt, a.ntile, nkeys(N));
+  if (e != cudaSuccess) return e;
+  if (keys) {
+    score_key_tiles_kernel<<<dim3((nkeys(N) + 7) / 8, B), 256, 0, st>>>(bounds, kt, a.ntile, nkeys(N));
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    score_order_kernel<<<1, kBins, 0, st>>>(kt, order, B, nkeys(N), 0, a.ntile, a.ntile);
+  } else {
+    score_order_kernel<<<1, kBins, 0, st>>>(bounds, order, B, (N + unit_rows - 1) / unit_rows, unit_rows / 64, a.ntile,
+                                            nkeys(N));
+  }
   return cudaGetLastError();
+}
+
+int score_mode(const int* row_ranges, const float* slopes, float cap) {
+  return (cap > 0.f ? kScoreCap : 0) | (slopes ? kScoreBias : 0) | (row_ranges ? kScoreRanges : 0);
 }
 
 }  // namespace
@@ -227,7 +288,7 @@ extern "C" attn_status attn_mask_rows(const int* doc_ids, const int* prefix_lens
 
 extern "C" size_t attn_score_workspace_size(int B, int N) {
   if (B < 1 || N < 1) return 0;
-  return round256(static_cast<size_t>(B) * (ntiles(N) * sizeof(int4) + nkeys(N) * sizeof(int2)));
+  return round256(static_cast<size_t>(B) * (ntiles(N) + 2 * static_cast<size_t>(nkeys(N))) * sizeof(int2));
 }
 
 extern "C" attn_status attn_fwd_score(const void* q, const void* k, const void* v, void* o, float* lse,
@@ -245,6 +306,10 @@ extern "C" attn_status attn_fwd_score(const void* q, const void* k, const void* 
   if (Hq % Hkv) return ATTN_ERR_GQA;
   if (dtype != ATTN_BF16 && dtype != ATTN_FP16) return ATTN_ERR_DTYPE;
   if (row_ranges && ws_bytes < attn_score_workspace_size(B, N)) return ATTN_ERR_WORKSPACE;
+  const int mode = score_mode(row_ranges, slopes, score_cap);
+  if (mode == 0)   // nothing modified
+    return attn_fwd_window(q, k, v, o, lse, B, Hq, Hkv, N, d, scale, window_left < N ? window_left : -1,
+                           window_right < N ? window_right : -1, dtype, stream);
   int* status;
   if ((s = device_context(&status)) != ATTN_OK) return s;
   CUtensorMap tq, tk, tv;
@@ -272,10 +337,10 @@ extern "C" attn_status attn_fwd_score(const void* q, const void* k, const void* 
   a.causal = !row_ranges && window_left < 0 && window_right == 0 ? 1 : 0;
   a.status = status;
   cudaError_t e = prepare_score(a.sc, row_ranges, slopes, scale, score_cap, B, N, window_left, window_right, workspace,
-                                false, st);
+                                fwd_unit_rows(d), false, st);
   if (e == cudaSuccess)
-    e = dtype == ATTN_BF16 ? launch_fwd_score_bf16(d, tq, tk, tv, a, N, Hq, B, st)
-                           : launch_fwd_score_fp16(d, tq, tk, tv, a, N, Hq, B, st);
+    e = dtype == ATTN_BF16 ? launch_fwd_score_bf16(mode, d, tq, tk, tv, a, N, Hq, B, st)
+                           : launch_fwd_score_fp16(mode, d, tq, tk, tv, a, N, Hq, B, st);
   return launch_status(e);
 }
 
@@ -293,6 +358,10 @@ extern "C" attn_status attn_bwd_score(const void* q, const void* k, const void* 
   if (s != ATTN_OK) return s;
   if ((s = check_score(row_ranges, slopes, scale, score_cap, N, window_left, window_right)) != ATTN_OK) return s;
   if (ws_bytes < attn_bwd_score_workspace_size(B, Hq, Hkv, N, d)) return ATTN_ERR_WORKSPACE;
+  const int mode = score_mode(row_ranges, slopes, score_cap);
+  if (mode == 0)
+    return attn_bwd_window(q, k, v, o, lse, dout, dq, dk, dv, workspace, ws_bytes, B, Hq, Hkv, N, d, scale,
+                           window_left < N ? window_left : -1, window_right < N ? window_right : -1, dtype, stream);
   int* status;
   if ((s = device_context(&status)) != ATTN_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -327,10 +396,13 @@ extern "C" attn_status attn_bwd_score(const void* q, const void* k, const void* 
   a.win_right = window_right;
   a.causal = !row_ranges && window_left < 0 && window_right == 0 ? 1 : 0;
   a.status = status;
-  cudaError_t e = prepare_score(a.sc, row_ranges, slopes, scale, score_cap, B, N, window_left, window_right, facts, true,
+  cudaError_t e = prepare_score(a.sc, row_ranges, slopes, scale, score_cap, B, N, window_left, window_right, facts, 0, true,
                                 st);
   if (e == cudaSuccess) e = launch_bwd_pre(dtype, d, o, dout, dvec, dq_acc, static_cast<long long>(rows), Hq, N, 0, st);
-  if (e == cudaSuccess) e = launch_bwd_score(dtype, d, tk, tv, tq, tdo, tdq, a, N, B, st);
+  if (e == cudaSuccess)
+    e = d == 64    ? launch_bwd_score_64(mode, dtype, tk, tv, tq, tdo, tdq, a, N, B, st)
+        : d == 128 ? launch_bwd_score_128(mode, dtype, tk, tv, tq, tdo, tdq, a, N, B, st)
+                   : launch_bwd_score_256(mode, dtype, tk, tv, tq, tdo, tdq, a, N, B, st);
   if (e == cudaSuccess) e = launch_dq_convert(dtype, dq_acc, dq, static_cast<long long>(rows) * d, scale, st);
   return launch_status(e);
 }

@@ -19,12 +19,17 @@
 
 namespace attn {
 
-// A score's sub-tile facts, per 64 rows: the union and the intersection of
-// the rows' visible keys. Row i's own are ranges[i] cut by the window.
+// What an instance of the kernels changes (their kScore parameter, a mask);
+// 0 is the plain kernel. Each has its own instances because a branch in the
+// softmax loops costs registers they do not have (one instance for all of
+// them ran the uncapped backward 27 % slower at d = 128).
+enum : int { kScoreCap = 1, kScoreBias = 2, kScoreRanges = 4 };
+
 struct ScoreArgs {
   const int2* ranges;       // [B, N] visible keys [x, y) of each row, or null
-  const int4* bounds;       // [B, ntile] per 64 rows: lowest lo, highest hi (of rows that see a key), highest lo, lowest hi
+  const int2* bounds;       // forward: [B, ntile] per 64 rows, the union of their visible keys
   const int2* key_tiles;    // backward: [B, ceil(N / 128)] 64-row tiles [x, y) that see a key of the 128
+  const int2* order;        // (tile, batch) of the units of one head, those with the most work first
   int ntile;                // ceil(N / 64)
   const float* slopes;      // [Hq] or null
   float sl2;                // scale * log2(e)
@@ -57,15 +62,21 @@ inline void set_cap(ScoreArgs& a, float scale, float cap) {
   }
 }
 
-// s -> cap_log2 tanh(s w_of_s) for a pair of scores with |w| <= 1 ...
-__device__ __forceinline__ float2 cap_pair(float2 s, float w_of_s, float cap_log2) {
+// s -> w and the factor q with q w = tanh(w), for a pair of scores with |w| <= 1
+__device__ __forceinline__ float2 cap_factor(float2 s, float w_of_s, float2& w) {
   constexpr float c[7] = {0.99999995f,   -0.333328392f,   0.133252041f,   -0.0534570296f,
                           0.0202899804f, -0.00620337911f, 0.00104102264f};   // degree 13
-  const float2 w = fmul2(s, make_float2(w_of_s, w_of_s));
+  w = fmul2(s, make_float2(w_of_s, w_of_s));
   const float2 z = fmul2(w, w);
   float2 q = make_float2(c[6], c[6]);
 #pragma unroll
   for (int i = 5; i >= 0; --i) q = ffma2(q, z, make_float2(c[i], c[i]));
+  return q;
+}
+// s -> cap_log2 tanh(s w_of_s), |w| <= 1 ...
+__device__ __forceinline__ float2 cap_pair(float2 s, float w_of_s, float cap_log2) {
+  float2 w;
+  const float2 q = cap_factor(s, w_of_s, w);
   return fmul2(fmul2(q, w), make_float2(cap_log2, cap_log2));
 }
 // ... and for any s
@@ -81,6 +92,13 @@ __device__ __forceinline__ float2 cap_small_factor(float2 s, const ScoreArgs& a)
   float2 q = ffma2(t, make_float2(a.k[3], a.k[3]), make_float2(a.k[2], a.k[2]));
   q = ffma2(t, q, make_float2(a.k[1], a.k[1]));
   return ffma2(t, q, make_float2(a.k[0], a.k[0]));
+}
+
+// one score by its tier's way
+__device__ __forceinline__ float cap_by(int tier, float s, const ScoreArgs& a) {
+  if (tier == 1) return s * cap_small_factor(make_float2(s, s), a).x;
+  if (tier == 2) return cap_pair(make_float2(s, s), a.w_of_s, a.cap_log2).x;
+  return cap_any(s, a.w_of_s, a.cap_log2);
 }
 
 // Visible keys of row i (in [0, N)): the row's range cut by the window.

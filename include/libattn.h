@@ -298,8 +298,8 @@ ATTN_API attn_status attn_rope_tables(float* rope_cos, float* rope_sin, const do
 ATTN_API attn_status attn_mask_rows(const int* doc_ids, const int* prefix_lens, int* row_ranges, int B, int N,
                                     int causal, void* stream);
 
-/* Bytes of workspace attn_fwd_score needs when row_ranges is given: 16 bytes
- * per 64 rows and 8 per 128, rounded up to 256. */
+/* Bytes of workspace attn_fwd_score needs when row_ranges is given: 8 bytes
+ * per 64 rows and 16 per 128 of each sequence, rounded up to 256. */
 ATTN_API size_t attn_score_workspace_size(int B, int N);
 
 /*

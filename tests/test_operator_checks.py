@@ -69,7 +69,7 @@ def test_score_refusals(lib):
     for b, n in ((0, 8), (65536, 8), (1, 0), (1, 2 ** 24 + 1)):
         assert lib.attn_mask_rows(P(), None, P(), b, n, 1, None) == 3
     w = L.attn_score_workspace_size(2, 300)
-    assert w == 256 and L.attn_score_workspace_size(2, 8192) == 2 * (128 * 16 + 64 * 8) and L.attn_score_workspace_size(0, 8) == 0
+    assert w == 256 and L.attn_score_workspace_size(2, 8192) == 2 * (128 * 8 + 64 * 16) and L.attn_score_workspace_size(0, 8) == 0
 
     def fwd(q=P(), lse=P(), ranges=None, slopes=None, ws=P(), wb=w, B=2, Hq=4, Hkv=2, N=300, d=64, scale=0.1, cap=0.0, left=-1,
             right=-1, dt=0):
