@@ -490,7 +490,7 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     // -------------------------------------------------------------- MMA
     // Order: SdP(0); per iteration it: SdP(it+1) into the other buffer, then
     // (after P^T/dS^T of it are ready) the two dQ^T halves, dV and dK of it.
-    if (lane == 0) {
+    if (elect_one()) {
       // Descriptors are built once; a byte offset is added to the
       // start-address field (16-byte units) for each K step and stage.
       const uint64_t dK_kmaj = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128);

@@ -109,6 +109,22 @@ struct FwdCfg {
   static constexpr int kPShift = 4;   // P~ <= 2^kTau, so P~ * 2^kPShift <= 256 < 448
 };
 
+// Two-tile instances with capped or biased scores give each query row two
+// threads, in warpgroups of their own, that take half of the keys each: the
+// longer way from score to weight is latency the softmax warps cannot hide
+// with one warp per query tile and scheduler . 640 threads: the load/MMA warpgroup keeps 64 registers, the four
+// softmax warpgroups have 104.
+template <int DT, int D, int QT, int kScore>
+struct FwdSplit {
+  using C = FwdCfg<DT, D, QT>;
+  static constexpr bool kRows = QT == 2 && (kScore & (kScoreCap | kScoreBias)) != 0;
+  static constexpr int NTHREADS = kRows ? 640 : C::NTHREADS;
+  static constexpr uint32_t kRegsCtl = kRows ? 64 : C::kRegsCtl, kRegsSoft = kRows ? 104 : C::kRegsSoft;
+  static_assert(!kRows || 128 * kRegsCtl + 512 * kRegsSoft <= 640 * 96, "register split");
+  static constexpr int XCH_B = kRows ? 2 * 2 * 128 * 4 : 0;   // row facts the two threads of a row exchange
+  static constexpr int SMEM_BYTES = C::SMEM_BYTES + XCH_B;
+};
+
 __device__ __forceinline__ int pow2_exponent_of(float x) {   // x an exact power of two
   return static_cast<int>((__float_as_uint(x) >> 23) & 0xFFu) - 127;
 }
@@ -221,10 +237,12 @@ __device__ __forceinline__ bool fwd_unit(const FwdArgs& a, int lin, FwdUnit& w) 
 // Biased scores walk the keys from the last to the first, so that the running
 // max starts near the row's own position, where the bias is least.
 template <int DT, int D, int QT, bool kPersist, int kScore = 0>
-__global__ void __launch_bounds__(FwdCfg<DT, D, QT>::NTHREADS, 1)
+__global__ void __launch_bounds__(FwdSplit<DT, D, QT, kScore>::NTHREADS, 1)
 fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
            const __grid_constant__ CUtensorMap tmV, const FwdArgs a) {
   using C = FwdCfg<DT, D, QT>;
+  using R = FwdSplit<DT, D, QT, kScore>;
+  static_assert(!R::kRows || !kPersist, "split rows: one unit per CTA");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
@@ -265,7 +283,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     }
     for (int t = 0; t < C::NSB; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_ready[t], 128);
+      mbar_init(&p_ready[t], R::kRows ? 256 : 128);
     }
     mbar_init(o_final, 1);
     mbar_init(o_done, 1);
@@ -290,7 +308,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
   // role changes its budget inside its own branch, so the compiler sizes
   // every role's code for the budget it runs with.
   if (warp < 4) {
-  if constexpr (QT == 2) regs_dec<C::kRegsCtl>();
+  if constexpr (QT == 2) regs_dec<R::kRegsCtl>();
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -342,7 +360,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t q_addr = smem_u32(sQ);
       const uint32_t kv_addr = smem_u32(sKV);
       int kvb = 0, gs = 0, ui = 0;   // K/V tiles, KV steps and units consumed before this unit
@@ -364,7 +382,9 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         for (int kk = 0; kk < 128 / C::KSTEP_E; ++kk) {
           const uint64_t bd = smem_desc(kv_addr + slot * C::TILE_B + kk * C::KSTEP_E * C::BOX_B,
                                         C::BOXT_B, C::SBO, C::SWZ);
-          mma_ts<C::kFp8>(tbase + C::O_COL + t * D, tbase + sb * 128 + kk * 8, bd, C::IDESC_O,
+          // split rows: the weights of keys 32c .. 32c + 31 stay in columns 32c .. 32c + 15
+          const uint32_t pcol = R::kRows ? (kk >> 1) * 32 + (kk & 1) * 8 : kk * 8;
+          mma_ts<C::kFp8>(tbase + C::O_COL + t * D, tbase + sb * 128 + pcol, bd, C::IDESC_O,
                           (j > 0 || kk > 0) ? 1u : 0u);
         }
       };
@@ -461,7 +481,115 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     __syncwarp();
   }
   } else {
-    if constexpr (QT == 2) regs_inc<C::kRegsSoft>();
+    if constexpr (QT == 2) regs_inc<R::kRegsSoft>();
+    if constexpr (R::kRows) {
+      // ------------------------------------------ softmax, two threads per row
+      constexpr bool kCap = (kScore & kScoreCap) != 0, kBias = (kScore & kScoreBias) != 0;
+      const int wg = (warp - 4) >> 2;
+      const int t = wg >> 1, part = wg & 1;           // query tile, half of the keys (and of the head dims)
+      const int quarter = warp & 3;
+      const int row = quarter * 32 + lane;
+      const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+      const uint32_t tO = tbase + lane_off + C::O_COL + t * D + part * (D / 2);
+      const uint32_t tS = tbase + lane_off + t * 128 + part * 64;
+      const uint32_t pair = 1 + t * 4 + quarter;      // named barrier of the two warps of these 32 rows
+      float* xch = reinterpret_cast<float*>(smem + C::SMEM_BYTES - 1024) + t * 256;   // [part][row]
+      FwdUnit w;
+      const bool unit = fwd_unit<QT, kScore>(a, fwd_unit_of(a, 0), w);   // true: checked above
+      const int L = w.L, qrow = (w.qt0 + t) * 128 + row;
+      int2 vis = make_int2(0, L);
+      if (qrow < L)
+        vis = score_row((kScore & kScoreRanges) ? a.sc.ranges : nullptr, static_cast<long long>(w.b) * L + qrow, qrow, L,
+                        a.win_left, a.win_right);
+      float slope2 = 0.f;
+      if constexpr (kBias) slope2 = __ldg(a.sc.slopes + w.h) * 1.4426950408889634f;
+      float m = -INFINITY, l = 0.f;
+      bool ok = unit;
+      for (int j = 0; j < w.nkv; ++j) {
+        const int kb = (w.kv0 + (kBias ? w.nkv - 1 - j : j)) * 128 + part * 64;   // first key of this half
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[t], j & 1, a.status));
+        tc_fence_after();
+        const bool edge = warp_any(vis.x > kb || vis.y < kb + 64);
+        ScoreTile st = score_bound<kCap, kBias, 2>(tS, a.sc, edge, slope2, kb - qrow);
+        // no visible score passes the running max by kTau, in either half of
+        // the warp's rows: it stays. (A wait that ran out ends both warps in
+        // the other branch.)
+        const bool none = vis.x >= kb + 64 || vis.y <= kb;
+        if (named_bar_and(pair, 64, ok && (none || st.top <= m + C::kTau))) {
+          if (!st.straight) score_finish<kCap, kBias, 2>(tS, a.sc, st.tier, edge, slope2, kb - qrow, vis.x - kb, vis.y - kb);
+        } else {
+          float mx = -INFINITY;
+          if (ok) {
+            if (kBias || !st.straight) {   // with a bias the largest raw score need not be the largest
+              st.straight = false;
+              mx = score_finish<kCap, kBias, 2>(tS, a.sc, st.tier, edge, slope2, kb - qrow, vis.x - kb, vis.y - kb);
+            } else {
+              mx = cap_by(st.tier, score_rowmax<false, 2>(tS), a.sc);
+            }
+          }
+          xch[part * 128 + row] = mx;
+          if (!(ok = named_bar_and(pair, 64, ok))) break;
+          mx = fmaxf(mx, xch[(part ^ 1) * 128 + row]);
+          float corr = 1.f;
+          if (mx > m + C::kTau) {
+            corr = ex2(m - mx);   // m = -inf gives 0
+            m = mx;
+          }
+          l *= corr;
+          if (j > 0 && warp_any(corr != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+              uint32_t r[32];
+              tmem_ld32(tO + 32 * c, r);
+              tmem_wait_ld();
+              reg_fence(r);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * corr);
+              tmem_st32(tO + 32 * c, r);
+            }
+          }
+        }
+        const float bias = m == -INFINITY ? 0.f : -m;
+        l += score_weights<DT == kBF16, kCap, kBias, 2>(tS, a.sc, st.straight ? st.tier : 0, slope2, kb - qrow, bias);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_ready[t]);
+      }
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_final, 0, a.status));
+      tc_fence_after();
+      if (ok) xch[part * 128 + row] = l;   // its last reads were before the step's barrier
+      if (named_bar_and(pair, 64, ok)) {
+        l += xch[(part ^ 1) * 128 + row];
+        const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees nothing: O = 0, LSE = -inf
+        const bool valid = qrow < L;
+        const long long row_off = static_cast<long long>(w.b) * a.o_sb + static_cast<long long>(w.h) * a.o_sh +
+                                  static_cast<long long>(qrow) * a.o_sn + part * (D / 2);
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t r[32];
+          tmem_ld32(tO + 32 * c, r);
+          tmem_wait_ld();
+          reg_fence(r);
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float x0 = __uint_as_float(r[2 * e]) * inv;
+            const float x1 = __uint_as_float(r[2 * e + 1]) * inv;
+            pk[e] = (DT == kFP16) ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
+          }
+          if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + row_off + 32 * c);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+          }
+        }
+        if (valid && part == 0) {
+          const float lse2 = (m == -INFINITY ? 0.f : m) + __log2f(l);
+          a.lse[static_cast<long long>(w.b) * a.l_sb + static_cast<long long>(w.h) * a.l_sh + qrow] =
+              lse2 * 0.69314718055994530942f;
+        }
+      }
+    } else {
     // ------------------------------------------------------- softmax
     const int t = (warp - 4) >> 2;
     const int quarter = warp & 3;
@@ -538,10 +666,17 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                  (a.win_left >= 0 && kb < qtile * 128 + 127 - a.win_left);
         }
         float mx = 0.f;             // largest score of the row (raw unless kChanged)
-        ScoreStep step{};
-        if constexpr (kChanged) {
-          step = score_step<kCap, kBias>(tS, a.sc, m + C::kTau, edge, slope2, kb - qrow, vis.x - kb, vis.y - kb);
-          mx = step.mx;
+        ScoreTile st{};
+        bool keep_max = false;
+        if constexpr (kChanged) {   // as with split rows, within one thread
+          st = score_bound<kCap, kBias, 4>(tS, a.sc, edge, slope2, kb - qrow);
+          const bool none = vis.x >= kb + 128 || vis.y <= kb;
+          keep_max = !warp_any(!(none || st.top <= m + C::kTau));
+          if (!keep_max && kBias) st.straight = false;
+          if (!st.straight)
+            mx = score_finish<kCap, kBias, 4>(tS, a.sc, st.tier, edge, slope2, kb - qrow, vis.x - kb, vis.y - kb);
+          else if (!keep_max)
+            mx = cap_by(st.tier, score_rowmax<false, 4>(tS), a.sc);
         } else {
           if (edge) {
             int hi, lo;                                                  // visible: lo <= c < hi
@@ -567,7 +702,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
           f_j = pow2_exponent_of(sv_j);
           f_new = max(f_run, f_j);
         }
-        if (!kChanged || !step.keep_max) {
+        if (!kChanged || !keep_max) {
           const float mxs = mx * sl2;
           const float m_new = (mxs > m + C::kTau) ? mxs : m;
           float corr = 1.f;
@@ -619,7 +754,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             tmem_st8(tS + 8 * c, pk);
           }
         } else if constexpr (kChanged) {
-          score_weights<DT == kBF16, kCap, kBias>(tS, a.sc, step.way, slope2, kb - qrow, bias, acc);
+          l += score_weights<DT == kBF16, kCap, kBias, 4>(tS, a.sc, st.straight ? st.tier : 0, slope2, kb - qrow, bias);
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -688,6 +823,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       }
       gs += nkv;
       ++ui;
+    }
     }
   }
   tc_fence_before();

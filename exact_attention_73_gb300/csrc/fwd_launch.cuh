@@ -23,13 +23,13 @@ inline bool fwd_persistent(int qt, const FwdArgs& a, int rows) {
 template <int DT, int D, int QT, bool kPersist, int kScore = 0>
 cudaError_t launch_fwd_grid(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const FwdArgs& u,
                             long long units, cudaStream_t st) {
-  using C = FwdCfg<DT, D, QT>;
+  using R = FwdSplit<DT, D, QT, kScore>;
   auto kern = fwd_kernel<DT, D, QT, kPersist, kScore>;
-  cudaError_t e = smem_attr_once<fwd_kernel<DT, D, QT, kPersist, kScore>>(C::SMEM_BYTES);
+  cudaError_t e = smem_attr_once<fwd_kernel<DT, D, QT, kPersist, kScore>>(R::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   if constexpr (QT >= 2) {   // the role split must fit the registers of the launch
-    constexpr int kSplit = (128 * C::kRegsCtl + 128 * QT * C::kRegsSoft + C::NTHREADS - 1) / C::NTHREADS;
-    if ((e = reg_pool_once<fwd_kernel<DT, D, QT, kPersist, kScore>>(C::NTHREADS, kSplit)) != cudaSuccess) return e;
+    constexpr int kSplit = (128 * R::kRegsCtl + (R::NTHREADS - 128) * R::kRegsSoft + R::NTHREADS - 1) / R::NTHREADS;
+    if ((e = reg_pool_once<fwd_kernel<DT, D, QT, kPersist, kScore>>(R::NTHREADS, kSplit)) != cudaSuccess) return e;
   }
   long long grid = units;
   if (kPersist) {
@@ -38,7 +38,7 @@ cudaError_t launch_fwd_grid(const CUtensorMap& q, const CUtensorMap& k, const CU
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     if (grid > sms) grid = sms;
   }
-  kern<<<static_cast<unsigned>(grid), C::NTHREADS, C::SMEM_BYTES, st>>>(q, k, v, u);
+  kern<<<static_cast<unsigned>(grid), R::NTHREADS, R::SMEM_BYTES, st>>>(q, k, v, u);
   return cudaGetLastError();
 }
 

