@@ -42,6 +42,7 @@ class AttnError(RuntimeError):
 
 
 _P, _I, _F, _Z = C.c_void_p, C.c_int, C.c_float, C.c_size_t
+_Strides = C.c_longlong * 3
 _S = C.POINTER(C.c_longlong)   # three element strides (batch, head, row) in host memory
 _SIGS = {
     "attn_status_string": ([_I], C.c_char_p),
@@ -112,17 +113,17 @@ def _ptr(t, name="tensor", numel=None, dtype=None, shape=None):
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.device.type != _DEVICE_TYPE:
+    if not t.is_cuda if _DEVICE_TYPE == "cuda" else t.device.type != _DEVICE_TYPE:
         raise ValueError(f"{name} must be a {_DEVICE_TYPE} tensor, not on {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (the library reads it as a dense array)")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} must hold {numel} elements, got {t.numel()}")
-    return C.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _dims(t, name, n):
@@ -151,7 +152,7 @@ def _bwd_ptrs(q, k, v, o, lse, dout, dq, dk, dv):
 def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
-    return C.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _check(code, where):
@@ -325,25 +326,31 @@ def attn_decode_fp8(q8, sq, k8, v8, sk, sv, o, lse, workspace, num_splits, seqle
 
 def _one_device(*tensors):
     """Every tensor on the current device: the stream and the library's launches are there."""
+    if _DEVICE_TYPE != "cuda":
+        return
+    current = None
     for t in tensors:
-        if isinstance(t, torch.Tensor) and t.device.type == "cuda" and t.device.index != torch.cuda.current_device():
-            raise ValueError(f"tensor on {t.device}, but cuda:{torch.cuda.current_device()} is the current device")
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            if current is None:
+                current = torch.cuda.current_device()
+            if t.get_device() != current:
+                raise ValueError(f"tensor on {t.device}, but cuda:{current} is the current device")
 
 
 def _strided(t, name, dtype=None, shape=None):
     """Pointer and strides of a [B, H, N, d] tensor whose rows are dense (any batch, head and row strides)."""
-    _dims(t, name, 4)
-    if t.device.type != _DEVICE_TYPE:
+    b, h, n, d = _dims(t, name, 4)
+    if not t.is_cuda if _DEVICE_TYPE == "cuda" else t.device.type != _DEVICE_TYPE:
         raise ValueError(f"{name} must be a {_DEVICE_TYPE} tensor, not on {t.device}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    sb, sh, sn, se = t.stride()
+    if d > 1 and se != 1:
         raise ValueError(f"{name} must have adjacent elements in each row (stride 1 in its last dimension)")
     # the stride of a dimension of size 1 is never used and may be anything
-    strides = (C.c_longlong * 3)(*(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)))
-    return C.c_void_p(t.data_ptr()), strides
+    return t.data_ptr(), _Strides(sb if b > 1 else 0, sh if h > 1 else 0, sn if n > 1 else 0)
 
 
 def _rope_dims(rope_cos, rope_sin):

@@ -762,30 +762,46 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
             }
           }
         }
-        // the bias joins -LSE: where every query lies at or behind every key
-        // it is linear, -slope (q - key), from one value per lane
-        const bool behind = q0 >= j * C::BC + quarter * 32 + 31;
-        const float from = static_cast<float>(q0 - kloc);
-        uint32_t pp[16], dd[16];
-        auto weights = [&](auto raw_scores) {
-          constexpr bool kRaw = decltype(raw_scores)::value;
-  #pragma unroll
-        for (int e4 = 0; e4 < 8; ++e4) {
-          float4 l4 = l4r[e4];
-          const float4 d4 = d4r[e4];
+        if constexpr (kScore != 0) {
+          // bias and mask join -LSE here, in blocks of their own, so that the
+          // loop below has no branch: p = exp2(x + l), and l = -inf hides a
+          // pair (as it does the queries past the sequence)
+          float* lf = reinterpret_cast<float*>(l4r);
           if constexpr (kBias) {
-            if (behind) {
-              const float2 f = make_float2(from, from), n = make_float2(-slope2, -slope2);
-              const float2 u = ffma2(n, fadd2(f, make_float2(4.f * e4, 4.f * e4 + 1.f)), make_float2(l4.x, l4.y));
-              const float2 w = ffma2(n, fadd2(f, make_float2(4.f * e4 + 2.f, 4.f * e4 + 3.f)), make_float2(l4.z, l4.w));
-              l4 = make_float4(u.x, u.y, w.x, w.y);
+            const float from = static_cast<float>(q0 - kloc);
+            if (q0 >= j * C::BC + quarter * 32 + 31) {   // every query at or behind every key of the warp: linear
+              const float at = -slope2 * from;
+              const float2 n = make_float2(-slope2, -slope2), at2 = make_float2(at, at);
+  #pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float2 v = fadd2(ffma2(n, make_float2(static_cast<float>(e), static_cast<float>(e + 1)), at2),
+                                       make_float2(lf[e], lf[e + 1]));
+                lf[e] = v.x;
+                lf[e + 1] = v.y;
+              }
             } else {
-              l4.x = fmaf(-slope2, fabsf(from + 4.f * e4), l4.x);
-              l4.y = fmaf(-slope2, fabsf(from + (4.f * e4 + 1.f)), l4.y);
-              l4.z = fmaf(-slope2, fabsf(from + (4.f * e4 + 2.f)), l4.z);
-              l4.w = fmaf(-slope2, fabsf(from + (4.f * e4 + 3.f)), l4.w);
+  #pragma unroll
+              for (int e = 0; e < 32; ++e) lf[e] = fmaf(-slope2, fabsf(from + static_cast<float>(e)), lf[e]);
             }
           }
+          if (edge) {
+  #pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int q = q0 + e;
+              const bool hide = kRanges ? !(seen >> e & 1u)
+                                        : !kvalid || (a.win_right >= 0 && kloc > q + a.win_right) ||
+                                              (a.win_left >= 0 && kloc < q - a.win_left);
+              if (hide) lf[e] = -INFINITY;
+            }
+          }
+        }
+        uint32_t pp[16], dd[16];
+        auto weights = [&](auto raw_scores) {
+          [[maybe_unused]] constexpr bool kRaw = decltype(raw_scores)::value;
+  #pragma unroll
+        for (int e4 = 0; e4 < 8; ++e4) {
+          const float4 l4 = l4r[e4];
+          const float4 d4 = d4r[e4];
           float2 s01 = make_float2(__uint_as_float(sv[4 * e4]), __uint_as_float(sv[4 * e4 + 1]));
           float2 s23 = make_float2(__uint_as_float(sv[4 * e4 + 2]), __uint_as_float(sv[4 * e4 + 3]));
           float2 x01, x23;
@@ -801,14 +817,10 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
             x23 = ffma2(s23, sl2v, make_float2(l4.z, l4.w));
           }
           float p[4] = {ex2(x01.x), ex2(x01.y), ex2(x23.x), ex2(x23.y)};
-          if (edge) {
+          if (kScore == 0 && edge) {
   #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const int q = q0 + 4 * e4 + u;
-              if constexpr (kRanges) {
-                if (!(seen >> (4 * e4 + u) & 1u)) p[u] = 0.f;
-                continue;
-              }
               if (!kvalid || (a.win_right >= 0 && kloc > q + a.win_right) || (a.win_left >= 0 && kloc < q - a.win_left))
                 p[u] = 0.f;
             }
@@ -819,11 +831,10 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                                    make_float2(d4.z, d4.w));
           float2 g01 = fmul2(make_float2(p[0], p[1]), t01);
           float2 g23 = fmul2(make_float2(p[2], p[3]), t23);
-          if constexpr (kCap) {
-            const float2 c2 = make_float2(a.sc.inv_cap2, a.sc.inv_cap2), one = make_float2(1.f, 1.f);
-            const float2 t0 = fmul2(s01, c2), t1 = fmul2(s23, c2);   // tanh
-            g01 = fmul2(g01, ffma2(make_float2(-t0.x, -t0.y), t0, one));
-            g23 = fmul2(g23, ffma2(make_float2(-t1.x, -t1.y), t1, one));
+          if constexpr (kCap) {   // 1 - tanh^2
+            const float2 c2 = make_float2(a.sc.neg_inv_cap2_sq, a.sc.neg_inv_cap2_sq), one = make_float2(1.f, 1.f);
+            g01 = fmul2(g01, ffma2(fmul2(s01, s01), c2, one));
+            g23 = fmul2(g23, ffma2(fmul2(s23, s23), c2, one));
           }
           if constexpr (DT == kBF16) {
             pp[2 * e4] = pack_bf16x2(p[0], p[1]);

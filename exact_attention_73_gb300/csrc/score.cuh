@@ -34,7 +34,7 @@ struct ScoreArgs {
   const float* slopes;      // [Hq] or null
   float sl2;                // scale * log2(e)
   float cap_log2;           // cap * log2(e), 0: no cap
-  float inv_cap2;           // 1 / cap_log2
+  float neg_inv_cap2_sq;    // -1 / cap_log2^2
   float w_of_s;             // scale / cap: the tanh's argument is s times this
   float s_small;            // |s| up to which the degree 7 polynomial is used
   float k[4];               // its coefficients in s^2, times scale * log2(e)
@@ -50,7 +50,7 @@ inline void set_cap(ScoreArgs& a, float scale, float cap) {
   const float log2e = 1.4426950408889634f;
   a.sl2 = scale * log2e;
   a.cap_log2 = cap * log2e;
-  a.inv_cap2 = cap > 0.f ? 1.f / a.cap_log2 : 0.f;
+  a.neg_inv_cap2_sq = cap > 0.f ? -1.f / (a.cap_log2 * a.cap_log2) : 0.f;
   a.w_of_s = cap > 0.f ? scale / cap : 0.f;
   const double w = std::fabs(static_cast<double>(a.w_of_s));
   const bool ok = w >= 1e-6 && w <= 1e4;
