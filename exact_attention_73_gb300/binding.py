@@ -149,8 +149,14 @@ def _bwd_ptrs(q, k, v, o, lse, dout, dq, dk, dv):
             _ptr(dv, "dv", k.numel(), dt)]
 
 
+# the current stream's handle without building a Stream object (4 us a call, as much as the launch itself)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 

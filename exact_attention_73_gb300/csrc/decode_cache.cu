@@ -34,6 +34,7 @@
 #include "lowp.cuh"
 #include "ops.h"
 #include "ptx.cuh"
+#include "score.cuh"
 
 namespace attn {
 
@@ -85,18 +86,34 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// The cache is read once: no room in L1 for it.
 template <int N>
 __device__ __forceinline__ void load_bytes(uint32_t (&w)[N / 4], const uint8_t* p) {   // N = 8 or 16
-  if constexpr (N == 16) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-  } else {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    w[0] = v.x; w[1] = v.y;
-  }
+  if constexpr (N == 16)
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+  else
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
 }
-// x * 2^e for any e that can occur (the factor need not be a float)
-__device__ __forceinline__ float scale_pow2(float x, int e) { return ldexpf(x, e); }
+// x * 2^e, |e| <= 252 (the factor itself need not be a float)
+__device__ __forceinline__ float scale_pow2(float x, int e) {
+  const int h = e >> 1;
+  return x * __int_as_float((h + 127) << 23) * __int_as_float((e - h + 127) << 23);
+}
+__device__ __forceinline__ int pow2_exponent(float x) {   // of a power of two, subnormal ones included
+  int e;
+  frexpf(x, &e);
+  return e - 1;
+}
+
+// x = 2 w log2(e) -> cap log2(e) tanh(w): by exp2 and a reciprocal, whose error
+// is of the cap's size, and for small w by the polynomial, so that a small
+// score keeps its own.
+__device__ __forceinline__ float cap_score(float x, float cap_log2) {
+  const float w = x * 0.34657359027997264f;   // ln 2 / 2
+  if (fabsf(w) <= 1.f) return cap_pair(make_float2(w, w), 1.f, cap_log2).x;
+  return cap_log2 - 2.f * cap_log2 * rcp_approx(1.f + ex2(x));
+}
 
 template <typename T, int D, int NR>
 __global__ void __launch_bounds__(32 * kWarps, (D == 256 ? 2 : NR == 2 ? 3 : 4))
@@ -108,6 +125,7 @@ decode_cache_kernel(const CacheDecArgs a) {
   extern __shared__ float smem[];                // [kWarps][8 NR][D] partial O, then m and l
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
+  if (a.splits > 1) grid_launch_dependents();   // the combine kernel may be set up
   int item = blockIdx.x;
   const int split = item % a.splits;
   item /= a.splits;
@@ -160,43 +178,60 @@ decode_cache_kernel(const CacheDecArgs a) {
   };
   load_set(blk0);
 
-  // K and V of the 16 keys of tile `tile` (128-key block tile / 8): rows past
-  // the visible keys stay zero, whatever the cache holds there
+  // The walk: units of 64 keys (half a block), every fourth one this warp's,
+  // in tiles of 16. All of it is the same in every lane.
+  const int unit_end = min(blk1 * 2, (L + 63) >> 6);
+  int unit = max(blk0 * 2, lo >> 6) + warp - kWarps, sub = 0, sub_end = 0;
+  float sk_u = 1.f, sv_u = 1.f;   // the unit's factors
+  const uint8_t *kp = a.k8, *vp = a.v8;   // this lane's first bytes of the tile
+  auto advance = [&]() -> bool {   // to the next tile; false past the last one
+    ++sub;
+    kp += 16 * D;
+    vp += 16 * D;
+    while (sub >= sub_end) {
+      unit += kWarps;
+      if (unit >= unit_end) return false;
+      const int blk = unit >> 1;
+      if (blk >= set0 + 32) load_set(blk);
+      const int page = __shfl_sync(0xffffffffu, page_l, blk - set0);
+      sk_u = __shfl_sync(0xffffffffu, sk_l, blk - set0);
+      sv_u = __shfl_sync(0xffffffffu, sv_l, blk - set0);
+      if (page < 0) continue;   // (sub_end is still reached)
+      sub = max(lo - unit * 64, 0) >> 4;
+      sub_end = (min(L - unit * 64, 64) + 15) >> 4;
+      const long long row = (a.table ? (static_cast<long long>(page) * a.Hkv + h) * 128
+                                     : (static_cast<long long>(b) * a.Hkv + h) * a.rows_max +
+                                           static_cast<long long>(blk) * 128) + (unit & 1) * 64 + sub * 16;
+      kp = a.k8 + (row + g) * D + 16 * t;
+      vp = a.v8 + (row + 2 * t) * D + VB * g;
+    }
+    return true;
+  };
+  // K and V of the tile's 16 keys; in a tile that is cut, rows that are not
+  // visible stay zero, whatever the cache holds there
   uint32_t kr[2][NG][4];          // keys g, g + 8
   uint32_t vr[4][NH][VB / 4];     // keys 2t, 2t + 1, 2t + 8, 2t + 9
-  auto block_base = [&](int tile) -> long long {   // byte offset of the tile's first row, -1: not there
-    const int blk = tile >> 3;
-    if (blk >= set0 + 32) load_set(blk);
-    const int page = __shfl_sync(0xffffffffu, page_l, blk - set0);
-    if (page < 0) return -1;
-    const long long row = a.table ? (static_cast<long long>(page) * a.Hkv + h) * 128
-                                  : (static_cast<long long>(b) * a.Hkv + h) * a.rows_max + static_cast<long long>(blk) * 128;
-    return (row + (tile & 7) * 16) * D;
-  };
-  auto load_k = [&](int tile, long long base) {
+  auto load_k = [&](int key0, bool cut) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int row = g + 8 * r, key = tile * 16 + row;
-      const bool in = base >= 0 && key >= lo && key < L;
+      const int key = key0 + g + 8 * r;
+      const bool in = !cut || (key >= lo && key < L);
 #pragma unroll
       for (int c = 0; c < NG; ++c) {
-        if (in) {
-          load_bytes<16>(kr[r][c], a.k8 + base + row * D + 64 * c + 16 * t);
-        } else {
-          kr[r][c][0] = kr[r][c][1] = kr[r][c][2] = kr[r][c][3] = 0;
-        }
+        if (in) load_bytes<16>(kr[r][c], kp + r * 8 * D + 64 * c);
+        else kr[r][c][0] = kr[r][c][1] = kr[r][c][2] = kr[r][c][3] = 0;
       }
     }
   };
-  auto load_v = [&](int tile, long long base) {
+  auto load_v = [&](int key0, bool cut) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int row = 2 * t + (r & 1) + 8 * (r >> 1), key = tile * 16 + row;
-      const bool in = base >= 0 && key >= lo && key < L;
+      const int row = (r & 1) + 8 * (r >> 1), key = key0 + 2 * t + row;
+      const bool in = !cut || (key >= lo && key < L);
 #pragma unroll
       for (int c = 0; c < NH; ++c) {
         if (in) {
-          load_bytes<VB>(vr[r][c], a.v8 + base + row * D + 128 * c + VB * g);
+          load_bytes<VB>(vr[r][c], vp + row * D + 128 * c);
         } else {
 #pragma unroll
           for (int i = 0; i < VB / 4; ++i) vr[r][c][i] = 0;
@@ -204,13 +239,17 @@ decode_cache_kernel(const CacheDecArgs a) {
       }
     }
   };
-  const int tile_end = min(blk1 * 8, (L + 15) >> 4);
-  int tile = max(blk0 * 8, lo >> 4) + warp;
-  long long base = -1;
-  if (tile < tile_end) {
-    base = block_base(tile);
-    load_k(tile, base);
-    load_v(tile, base);
+  bool more = advance();
+  int key0 = unit * 64 + sub * 16;   // the tile's first key
+  bool cut = key0 < lo || key0 + 16 > L;
+  if (more) {
+    if (cut) {
+      load_k(key0, true);
+      load_v(key0, true);
+    } else {
+      load_k(key0, false);
+      load_v(key0, false);
+    }
   }
 
   // Q^T fragments: head g (of each eight), the dims of this lane's K bytes
@@ -272,12 +311,12 @@ decode_cache_kernel(const CacheDecArgs a) {
       l[n][u] = 0.f;
     }
   }
-  int f_cur = 0;                  // O is held in units of 2^f_cur
-  bool first = true;
+  float s_cur = 0.f;              // O is held in units of this factor (0: none yet)
 
-  for (; tile < tile_end; tile += kWarps) {
-    const int blk = tile >> 3;
-    const float sk = __shfl_sync(0xffffffffu, sk_l, blk - set0), sv = __shfl_sync(0xffffffffu, sv_l, blk - set0);
+  while (more) {
+    const float sk = sk_u, sv = sv_u;
+    const int key = key0 + g;
+    const bool edge = cut;
     float s[NR][4];
 #pragma unroll
     for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
@@ -290,26 +329,23 @@ decode_cache_kernel(const CacheDecArgs a) {
 #pragma unroll
         for (int n = 0; n < NR; ++n) mma_16816(s[n], a0, a1, a2, a3, qf[n][c][w][0], qf[n][c][w][1]);
       }
-    const bool here = base >= 0;
-    const int next = tile + kWarps;
-    const bool more = next < tile_end;
-    long long base_next = -1;
+    more = advance();   // the next tile's loads go out as the registers come free
+    key0 = unit * 64 + sub * 16;
+    cut = key0 < lo || key0 + 16 > L;
     if (more) {
-      base_next = block_base(next);
-      load_k(next, base_next);
+      if (cut) load_k(key0, true);
+      else load_k(key0, false);
     }
     // scores in log2 units: values 0, 1 are key g, values 2, 3 key g + 8, of heads 2t and 2t + 1
-    const int key0 = tile * 16 + g;
-    const bool edge = !here || tile * 16 < lo || tile * 16 + 16 > L;
 #pragma unroll
     for (int n = 0; n < NR; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float x = s[n][e] * (qscale[n][e & 1] * sk);
-        if (a.cap > 0.f) x = a.cap_log2 - 2.f * a.cap_log2 * rcp_approx(1.f + ex2(x));   // cap tanh(z), x = 2 z log2(e)
-        const int key = key0 + 8 * (e >> 1);
-        if (a.slopes) x -= slope2[n][e & 1] * static_cast<float>(L - 1 - key);
-        if (edge && (!here || key < lo || key >= L)) x = -INFINITY;
+        if (a.cap > 0.f) x = cap_score(x, a.cap_log2);
+        const int at = key + 8 * (e >> 1);
+        if (a.slopes) x -= slope2[n][e & 1] * static_cast<float>(L - 1 - at);
+        if (edge && (at < lo || at >= L)) x = -INFINITY;
         s[n][e] = x;
       }
     // move the running max where a score passes it by more than kTau
@@ -339,18 +375,17 @@ decode_cache_kernel(const CacheDecArgs a) {
           }
         }
     }
-    const int f_j = static_cast<int>((__float_as_uint(sv) >> 23) & 0xffu) - 127;
-    if (here && (first || f_j != f_cur)) {   // a block with another V factor: O to its units
-      if (!first) {
+    if (sv != s_cur) {   // a block with another V factor: O to its units
+      if (s_cur != 0.f) {
+        const int e = max(-252, min(252, pow2_exponent(s_cur) - pow2_exponent(sv)));
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
           for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][i][e] = scale_pow2(acc[n][i][e], f_cur - f_j);
+            for (int u = 0; u < 4; ++u) acc[n][i][u] = scale_pow2(acc[n][i][u], e);
       }
-      f_cur = f_j;
-      first = false;
+      s_cur = sv;
     }
     uint32_t pb[NR][2];
 #pragma unroll
@@ -380,8 +415,10 @@ decode_cache_kernel(const CacheDecArgs a) {
           mma_16816(acc[n][i + 1], b0, b1, b2, b3, pb[n][0], pb[n][1]);
         }
       }
-    if (more) load_v(next, base_next);
-    base = base_next;
+    if (more) {
+      if (cut) load_v(key0, true);
+      else load_v(key0, false);
+    }
   }
 
   // join the warps: the largest m, then sums of O and l at it
@@ -413,8 +450,8 @@ decode_cache_kernel(const CacheDecArgs a) {
       for (int i = 0; i < MT; ++i) {
         // tile i holds head dims (chunk base of lane group g) + 2 (i mod tiles per half), + 1
         const int dim = (i / (VB / 2)) * 128 + VB * g + 2 * (i % (VB / 2));
-        *reinterpret_cast<float2*>(dst + dim) = make_float2(scale_pow2(acc[n][i][u] * corr, f_cur),
-                                                            scale_pow2(acc[n][i][2 + u] * corr, f_cur));
+        *reinterpret_cast<float2*>(dst + dim) = make_float2(acc[n][i][u] * corr * s_cur,
+                                                            acc[n][i][2 + u] * corr * s_cur);
       }
     }
   __syncthreads();
@@ -447,28 +484,56 @@ decode_cache_kernel(const CacheDecArgs a) {
   }
 }
 
-// One CTA per (sequence, query head), one thread per two head dims.
-template <typename T>
+// One warp per (sequence, query head), D / 32 head dims per lane. Lane i has
+// split i's log-sum-exp (of each 32), so the splits' partial rows can be
+// loaded one behind the other without waiting.
+template <typename T, int D>
 __global__ void __launch_bounds__(128) combine_kernel(const float* __restrict__ o_part, const float* __restrict__ lse_part,
-                                                      T* __restrict__ o, float* __restrict__ lse, int splits, int rows,
-                                                      int d) {
-  const int r = blockIdx.x, t = threadIdx.x;
+                                                      T* __restrict__ o, float* __restrict__ lse, int splits, int rows) {
+  grid_wait_prerequisites();   // launched while the splits' kernel runs
+  constexpr int N = D / 32, V = N < 4 ? N : 4;
+  const int r = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= rows) return;
   float mx = -INFINITY;
-  for (int s = 0; s < splits; ++s) mx = fmaxf(mx, lse_part[static_cast<long long>(s) * rows + r]);
-  float tot = 0.f, x = 0.f, y = 0.f;
-  for (int s = 0; s < splits; ++s) {
-    const float z = lse_part[static_cast<long long>(s) * rows + r];
-    if (z == -INFINITY) continue;   // nothing seen: its O was not written
-    const float w = expf(z - mx);
-    const float2 v = *reinterpret_cast<const float2*>(o_part + (static_cast<long long>(s) * rows + r) * d + 2 * t);
-    tot += w;
-    x += w * v.x;
-    y += w * v.y;
+  for (int s = lane; s < splits; s += 32) mx = fmaxf(mx, lse_part[static_cast<long long>(s) * rows + r]);
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
+  float tot = 0.f, x[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = 0.f;
+  for (int s0 = 0; s0 < splits; s0 += 32) {
+    const float z = s0 + lane < splits ? lse_part[static_cast<long long>(s0 + lane) * rows + r] : -INFINITY;
+    const float w_l = z == -INFINITY ? 0.f : expf(z - mx);
+    tot += w_l;
+    const int n = min(32, splits - s0);
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float w = __shfl_sync(0xffffffffu, w_l, s);
+      if (w == 0.f) continue;   // nothing seen (its O was not written), or nothing that counts
+      const float* src = o_part + (static_cast<long long>(s0 + s) * rows + r) * D + lane * V;
+#pragma unroll
+      for (int c = 0; c < N / V; ++c) {
+        float v[V];
+        if constexpr (V == 4) *reinterpret_cast<float4*>(v) = __ldcs(reinterpret_cast<const float4*>(src + 128 * c));
+        else *reinterpret_cast<float2*>(v) = __ldcs(reinterpret_cast<const float2*>(src));
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[c * V + i] = fmaf(w, v[i], x[c * V + i]);
+      }
+    }
   }
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, i);
   const float inv = tot > 0.f ? 1.f / tot : 0.f;
-  const uint32_t pk = std::is_same<T, __nv_bfloat16>::value ? pack_bf16x2(x * inv, y * inv) : pack_f16x2(x * inv, y * inv);
-  *reinterpret_cast<uint32_t*>(o + static_cast<long long>(r) * d + 2 * t) = pk;
-  if (t == 0) lse[r] = mx == -INFINITY ? -INFINITY : mx + logf(tot);
+  T* dst = o + static_cast<long long>(r) * D + lane * V;
+#pragma unroll
+  for (int c = 0; c < N / V; ++c)
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float p = x[c * V + i] * inv, q = x[c * V + i + 1] * inv;
+      *reinterpret_cast<uint32_t*>(dst + 128 * c + i) =
+          std::is_same<T, __nv_bfloat16>::value ? pack_bf16x2(p, q) : pack_f16x2(p, q);
+    }
+  if (lane == 0) lse[r] = mx == -INFINITY ? -INFINITY : mx + logf(tot);
 }
 
 template <typename T, int D, int NR>
@@ -479,9 +544,19 @@ cudaError_t launch_decode(const CacheDecArgs& a, cudaStream_t st) {
   const long long grid = static_cast<long long>(a.B) * a.Hkv * a.row_groups * a.splits;
   decode_cache_kernel<T, D, NR><<<static_cast<unsigned>(grid), 32 * kWarps, SMEM, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
-  combine_kernel<T><<<static_cast<unsigned>(a.B * a.Hq), D / 2, 0, st>>>(a.o_part, a.lse_part, static_cast<T*>(a.o),
-                                                                         a.lse, a.splits, a.B * a.Hq, D);
-  return cudaGetLastError();
+  // a programmatic dependent: its launch overlaps the splits' kernel, whose results it waits for
+  const int rows = a.B * a.Hq;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<T, D>, static_cast<const float*>(a.o_part),
+                            static_cast<const float*>(a.lse_part), static_cast<T*>(a.o), a.lse, a.splits, rows);
 }
 
 template <typename T>
