@@ -23,9 +23,16 @@
 // block's V factor; both rescales are rare. Q is scaled per head to fill FP16
 // (a power of two: BF16's 8 and FP16's 11 bits stay exact).
 //
-// A CTA is one (split, 8 or 16 heads of a KV head, sequence); its four warps
-// take every fourth 16-key tile of the split and meet once, at the end. A
-// second kernel combines the splits by their log-sum-exp weights.
+// The work is the visible 128-key blocks of all items (8 or 16 heads of a KV
+// head of a sequence), laid end to end; the grid fills the GPU once and every
+// CTA takes an equal run of blocks, whatever the lengths: a run may cover
+// parts of several items, an item may be cut into pieces (short runs: one
+// piece of one item each). (A fixed number of
+// pieces per item, each a CTA, leaves a part of a wave idle: 16 caches of
+// 32768 tokens took 186 to 266 us depending on that number, ragged lengths
+// 33 to 98 us.) A CTA's four warps take every fourth 64 keys of a piece
+// and meet once, at its end. A second kernel combines the pieces of an item
+// by their log-sum-exp weights.
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -43,6 +50,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTau = 8.f;      // the running max is left behind by up to this (log2 units)
+constexpr int kEvenRun = 16;     // blocks per CTA from which runs are cut without regard to items
 constexpr float kPShift = 7.f;   // P~ = 2^7 exp2(x - m) <= 2^15
 
 struct CacheDecArgs {
@@ -56,9 +64,12 @@ struct CacheDecArgs {
   const float* slopes;       // [Hq] or null
   void* o;                   // [B, Hq, d]
   float* lse;                // [B, Hq]
-  float* o_part;             // [splits][B * Hq][d]
+  float* o_part;             // [splits][B * Hq][d], by piece
   float* lse_part;           // [splits][B * Hq]
-  int B, Hq, Hkv, group, rows_max, blocks, pages, splits, blocks_per_split, row_groups;
+  int* pieces;               // [B][Hkv][row_groups] pieces of each item that has a block
+  int B, Hq, Hkv, group, rows_max, blocks, pages, row_groups;
+  int splits;                // pieces an item may have (1: an item is a CTA's)
+  int min_quota;             // blocks per CTA, at least, for that
   float scale_log2;          // scale * log2(e)
   float cap, cap_log2, inv_cap;   // cap (0: none), cap * log2(e), 2 log2(e) * scale / cap
   int window;                // keys before L - 1 - window are hidden (-1: none)
@@ -115,39 +126,55 @@ __device__ __forceinline__ float cap_score(float x, float cap_log2) {
   return cap_log2 - 2.f * cap_log2 * rcp_approx(1.f + ex2(x));
 }
 
+// CTAs per SM the kernel is built for.
+template <int D, int NR>
+constexpr int decode_ctas() { return D == 256 ? 2 : NR == 2 ? 3 : 4; }
+
+// Visible keys [x, y) of a sequence.
+__device__ __forceinline__ int2 visible_keys(const CacheDecArgs& a, int b) {
+  const int L = max(0, min(a.seqlens[b], a.rows_max));
+  return make_int2(a.window >= 0 ? max(0, L - 1 - a.window) : 0, L);
+}
+__device__ __forceinline__ int visible_blocks(int2 k) { return k.x < k.y ? ((k.y + 127) >> 7) - (k.x >> 7) : 0; }
+
+// Sum over the CTA (every thread gets it).
+__device__ __forceinline__ long long cta_sum(long long x, long long* scratch) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  __syncthreads();            // scratch was read
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) x += scratch[w];
+  return x;
+}
+
+// Blocks blk0 .. blk1 - 1 of one item: `piece` of `pieces`.
 template <typename T, int D, int NR>
-__global__ void __launch_bounds__(32 * kWarps, (D == 256 ? 2 : NR == 2 ? 3 : 4))
-decode_cache_kernel(const CacheDecArgs a) {
+__device__ __forceinline__ void decode_piece(const CacheDecArgs& a, float* smem, int b, int h, int rg, int lo, int L,
+                                             int blk0, int blk1, int piece, int pieces) {
   constexpr int NG = D / 64;                     // 64-dim groups of the K contraction
   constexpr int VB = D == 64 ? 8 : 16;           // bytes of a V row per lane and half
   constexpr int NH = D == 256 ? 2 : 1;           // halves of a V row
   constexpr int MT = D / 16;                     // 16-dim tiles of O^T
-  extern __shared__ float smem[];                // [kWarps][8 NR][D] partial O, then m and l
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  if (a.splits > 1) grid_launch_dependents();   // the combine kernel may be set up
-  int item = blockIdx.x;
-  const int split = item % a.splits;
-  item /= a.splits;
-  const int rg = item % a.row_groups;
-  item /= a.row_groups;
-  const int h = item % a.Hkv, b = item / a.Hkv;
   const int head0 = rg * 8 * NR;                 // first head of the KV head's group in this CTA
   const int heads = min(a.group - head0, 8 * NR);
   const long long qrow0 = static_cast<long long>(b) * a.Hq + static_cast<long long>(h) * a.group + head0;
-  // visible keys [lo, L) and this split's blocks of them
-  const int L = max(0, min(a.seqlens[b], a.rows_max));
-  const int lo = a.window >= 0 ? max(0, L - 1 - a.window) : 0;
-  const int blk0 = (lo >> 7) + split * a.blocks_per_split;
-  const int blk1 = min((L + 127) >> 7, blk0 + a.blocks_per_split);
-  if (blk0 >= blk1) {   // nothing to see in this split
-    if (a.splits > 1) {
-      if (threadIdx.x < heads) a.lse_part[static_cast<long long>(split) * a.B * a.Hq + qrow0 + threadIdx.x] = -INFINITY;
-    } else {
-      for (int i = threadIdx.x; i < heads * D; i += 32 * kWarps) static_cast<T*>(a.o)[qrow0 * D + i] = T(0.f);
-      if (threadIdx.x < heads) a.lse[qrow0 + threadIdx.x] = -INFINITY;
-    }
-    return;
+
+  // the query's rows first: they wait for nothing
+  uint4 qw[NR][NG][2];
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    const T* q = static_cast<const T*>(a.q) + (qrow0 + 8 * n + g) * D;
+#pragma unroll
+    for (int c = 0; c < NG; ++c)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        qw[n][c][u] = 8 * n + g < heads ? __ldg(reinterpret_cast<const uint4*>(q + 64 * c + 16 * t) + u)
+                                        : make_uint4(0, 0, 0, 0);
   }
 
   // block facts, held by the lanes: lane i has block set0 + i
@@ -258,17 +285,13 @@ decode_cache_kernel(const CacheDecArgs a) {
   float slope2[NR][2];            // slope * log2(e) of the same heads
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
-    const bool in = 8 * n + g < heads;
-    const T* q = static_cast<const T*>(a.q) + (qrow0 + 8 * n + g) * D;
-    uint4 w[NG][2];
     float amax = 0.f;
 #pragma unroll
     for (int c = 0; c < NG; ++c)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        w[c][u] = in ? __ldg(reinterpret_cast<const uint4*>(q + 64 * c + 16 * t) + u) : make_uint4(0, 0, 0, 0);
         float f[8];
-        unpack8<T>(w[c][u], f);
+        unpack8<T>(qw[n][c][u], f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
       }
@@ -282,7 +305,7 @@ decode_cache_kernel(const CacheDecArgs a) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         float f[8];
-        unpack8<T>(w[c][u], f);
+        unpack8<T>(qw[n][c][u], f);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           qf[n][c][2 * u + (i >> 1)][i & 1] = pack_f16x2(scale_pow2(f[2 * i], ex), scale_pow2(f[2 * i + 1], ex));
@@ -472,8 +495,8 @@ decode_cache_kernel(const CacheDecArgs a) {
     const float inv = tot > 0.f ? 1.f / tot : 0.f;   // every block missing: O = 0
     const float z = mx == -INFINITY ? -INFINITY : (mx + log2f(tot) - kPShift) * 0.69314718055994530942f;
     const long long row = qrow0 + col;
-    if (a.splits > 1) {
-      const long long pr = static_cast<long long>(split) * a.B * a.Hq + row;
+    if (pieces > 1) {
+      const long long pr = static_cast<long long>(piece) * a.B * a.Hq + row;
       *reinterpret_cast<float2*>(a.o_part + pr * D + dim) = make_float2(x * inv, y * inv);
       if (dim == 0) a.lse_part[pr] = z;
     } else {
@@ -484,16 +507,149 @@ decode_cache_kernel(const CacheDecArgs a) {
   }
 }
 
+template <typename T, int D, int NR>
+__global__ void __launch_bounds__(32 * kWarps, (decode_ctas<D, NR>()))
+decode_cache_kernel(const CacheDecArgs a) {
+  extern __shared__ float smem[];                // [kWarps][8 NR][D] partial O, then m and l
+  __shared__ long long sh_scan[kWarps], sh_start;
+  __shared__ int sh_b;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per_seq = a.Hkv * a.row_groups;      // items per sequence
+  // `at`: where this CTA stands, in units of the way the work is dealt.
+  // kWhole (one split): items, round-robin. kCut: blocks of the total, an even
+  // run per CTA wherever items begin. kPieces, for short runs, where a second
+  // piece would cost a CTA more than it evens out: pieces of at most `size`
+  // blocks, the smallest size that needs no more CTAs than there are.
+  enum { kWhole, kCut, kPieces };
+  int way = kWhole, size = 1;
+  int n = 0;                  // blocks of sequence threadIdx.x of the 128 looked at
+  long long at = blockIdx.x, end = static_cast<long long>(a.B) * per_seq, quota = 1;
+  if (a.splits > 1) {
+    grid_launch_dependents();   // the combine kernel may be set up
+    long long total = 0;
+    for (int b = threadIdx.x; b < a.B; b += 32 * kWarps) total += n = visible_blocks(visible_keys(a, b));
+    total = cta_sum(total, sh_scan) * per_seq;
+    const long long even = (total + gridDim.x - 1) / gridDim.x;   // blocks per CTA
+    if (even >= kEvenRun) {
+      way = kCut;
+      quota = max(even, static_cast<long long>(a.min_quota));
+      at = blockIdx.x * quota;
+      end = min(at + quota, total);
+    } else {
+      way = kPieces;
+      end = LLONG_MAX;
+      size = max(a.min_quota, 1);
+      int hi = max(size, a.blocks);   // whole items
+      while (size < hi) {
+        const int mid = (size + hi) >> 1;
+        long long c = 0;
+        if (a.B <= 32 * kWarps) c = (n + mid - 1) / mid;
+        else
+          for (int b = threadIdx.x; b < a.B; b += 32 * kWarps) c += (visible_blocks(visible_keys(a, b)) + mid - 1) / mid;
+        if (cta_sum(c, sh_scan) * per_seq <= gridDim.x) hi = mid;
+        else size = mid + 1;
+      }
+    }
+  }
+  int b0 = 0;                 // the sequences looked at: b0 .. b0 + 127
+  long long before = 0;       // weight of those before: blocks (kCut) or pieces of an item (kPieces)
+  for (; at < end; __syncthreads()) {   // smem is the next piece's
+    int b, i, piece = 0, pieces = 1, blk0, blk1;
+    int2 k;
+    if (way == kWhole) {
+      b = static_cast<int>(at / per_seq);
+      i = static_cast<int>(at % per_seq);
+      k = visible_keys(a, b);
+      blk0 = k.x >> 7;
+      blk1 = k.x < k.y ? (k.y + 127) >> 7 : blk0;
+      at += gridDim.x;
+    } else {
+      // the sequence that `at` lies in
+      if (threadIdx.x == 0) sh_b = -1;
+      while (true) {
+        if (a.B > 32 * kWarps)
+          n = b0 + static_cast<int>(threadIdx.x) < a.B ? visible_blocks(visible_keys(a, b0 + threadIdx.x)) : 0;
+        const int wt = way == kCut ? n : (n + size - 1) / size;
+        long long incl = wt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        __syncthreads();      // sh_scan was read, sh_b is set
+        if (lane == 31) sh_scan[warp] = incl;
+        __syncthreads();
+        long long first = before + incl - wt, all = 0;
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < warp) first += sh_scan[w];
+          all += sh_scan[w];
+        }
+        if (wt > 0 && at >= first * per_seq && at < (first + wt) * per_seq) {
+          sh_b = b0 + threadIdx.x;
+          sh_start = first * per_seq;
+        }
+        __syncthreads();
+        if (sh_b >= 0) break;
+        b0 += 32 * kWarps;
+        before += all;
+        if (b0 >= a.B) return;   // no piece is left
+      }
+      b = sh_b;
+      const long long in = at - sh_start;   // units into the sequence
+      k = visible_keys(a, b);
+      const int nb = visible_blocks(k);
+      if (way == kCut) {
+        i = static_cast<int>(in / nb);
+        const int off = static_cast<int>(in % nb);
+        const int take = static_cast<int>(min(static_cast<long long>(nb - off), end - at));
+        const long long item0 = at - off, first = item0 / quota;   // the CTA of the item's first block
+        piece = static_cast<int>(blockIdx.x - first);
+        pieces = static_cast<int>((item0 + nb - 1) / quota - first) + 1;
+        blk0 = (k.x >> 7) + off;
+        blk1 = blk0 + take;
+        at += take;
+      } else {
+        const int cnt = (nb + size - 1) / size, len = (nb + cnt - 1) / cnt;   // as even as whole blocks go
+        i = static_cast<int>(in / cnt);
+        piece = static_cast<int>(in % cnt);
+        pieces = (nb + len - 1) / len;
+        blk0 = (k.x >> 7) + piece * len;
+        blk1 = min(blk0 + len, (k.y + 127) >> 7);
+        at += gridDim.x;
+      }
+      if (piece == 0 && threadIdx.x == 0) a.pieces[static_cast<long long>(b) * per_seq + i] = pieces;
+    }
+    const int h = i / a.row_groups, rg = i % a.row_groups;
+    if (blk0 < blk1) {
+      decode_piece<T, D, NR>(a, smem, b, h, rg, k.x, k.y, blk0, blk1, piece, pieces);
+    } else if (way == kWhole) {   // a sequence without keys
+      const int head0 = rg * 8 * NR, heads = min(a.group - head0, 8 * NR);
+      const long long row = static_cast<long long>(b) * a.Hq + static_cast<long long>(h) * a.group + head0;
+      for (int e = threadIdx.x; e < heads * D; e += 32 * kWarps) static_cast<T*>(a.o)[row * D + e] = T(0.f);
+      if (threadIdx.x < heads) a.lse[row + threadIdx.x] = -INFINITY;
+    }
+  }
+}
+
 // One warp per (sequence, query head), D / 32 head dims per lane. Lane i has
 // split i's log-sum-exp (of each 32), so the splits' partial rows can be
 // loaded one behind the other without waiting.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) combine_kernel(const float* __restrict__ o_part, const float* __restrict__ lse_part,
-                                                      T* __restrict__ o, float* __restrict__ lse, int splits, int rows) {
-  grid_wait_prerequisites();   // launched while the splits' kernel runs
+template <typename T, int D, int NR>
+__global__ void __launch_bounds__(128) combine_kernel(const CacheDecArgs a) {
   constexpr int N = D / 32, V = N < 4 ? N : 4;
+  const int rows = a.B * a.Hq;
   const int r = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const float* __restrict__ o_part = a.o_part;
+  const float* __restrict__ lse_part = a.lse_part;
+  int splits = 0;
+  const int b = r < rows ? r / a.Hq : 0, hq = r - b * a.Hq, h = hq / a.group;
+  const int item = (b * a.Hkv + h) * a.row_groups + (hq - h * a.group) / (8 * NR);
+  grid_wait_prerequisites();   // launched while the pieces' kernel runs
   if (r >= rows) return;
+  if (a.seqlens[b] > 0) {
+    splits = a.pieces[item];
+    if (splits == 1) return;   // written already
+  }
   float mx = -INFINITY;
   for (int s = lane; s < splits; s += 32) mx = fmaxf(mx, lse_part[static_cast<long long>(s) * rows + r]);
 #pragma unroll
@@ -524,7 +680,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const float* __restrict__ 
 #pragma unroll
   for (int i = 16; i > 0; i >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, i);
   const float inv = tot > 0.f ? 1.f / tot : 0.f;
-  T* dst = o + static_cast<long long>(r) * D + lane * V;
+  T* dst = static_cast<T*>(a.o) + static_cast<long long>(r) * D + lane * V;
 #pragma unroll
   for (int c = 0; c < N / V; ++c)
 #pragma unroll
@@ -533,7 +689,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const float* __restrict__ 
       *reinterpret_cast<uint32_t*>(dst + 128 * c + i) =
           std::is_same<T, __nv_bfloat16>::value ? pack_bf16x2(p, q) : pack_f16x2(p, q);
     }
-  if (lane == 0) lse[r] = mx == -INFINITY ? -INFINITY : mx + logf(tot);
+  if (lane == 0) a.lse[r] = mx == -INFINITY ? -INFINITY : mx + logf(tot);
 }
 
 template <typename T, int D, int NR>
@@ -541,13 +697,17 @@ cudaError_t launch_decode(const CacheDecArgs& a, cudaStream_t st) {
   constexpr int SMEM = (kWarps * 8 * NR * D + 2 * kWarps * 8 * NR) * 4;
   cudaError_t e = smem_attr_once<decode_cache_kernel<T, D, NR>>(SMEM);
   if (e != cudaSuccess) return e;
-  const long long grid = static_cast<long long>(a.B) * a.Hkv * a.row_groups * a.splits;
-  decode_cache_kernel<T, D, NR><<<static_cast<unsigned>(grid), 32 * kWarps, SMEM, st>>>(a);
+  int dev = 0, sms = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  // one CTA per place on the GPU, and none that cannot get a block (an item)
+  const long long most = static_cast<long long>(a.B) * a.Hkv * a.row_groups * (a.splits == 1 ? 1 : a.blocks);
+  const long long places = static_cast<long long>(sms) * decode_ctas<D, NR>();
+  decode_cache_kernel<T, D, NR><<<static_cast<unsigned>(most < places ? most : places), 32 * kWarps, SMEM, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
-  // a programmatic dependent: its launch overlaps the splits' kernel, whose results it waits for
-  const int rows = a.B * a.Hq;
+  // a programmatic dependent: its launch overlaps the pieces' kernel, whose results it waits for
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
+  cfg.gridDim = dim3(static_cast<unsigned>((a.B * a.Hq + 3) / 4));
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -555,8 +715,7 @@ cudaError_t launch_decode(const CacheDecArgs& a, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<T, D>, static_cast<const float*>(a.o_part),
-                            static_cast<const float*>(a.lse_part), static_cast<T*>(a.o), a.lse, a.splits, rows);
+  return cudaLaunchKernelEx(&cfg, combine_kernel<T, D, NR>, a);
 }
 
 template <typename T>
@@ -582,14 +741,16 @@ extern "C" int attn_decode_cache_fp8_splits(int B, int Hq, int Hkv, int blocks) 
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || blocks < 1) return 0;
   const int group = Hq / Hkv, per = heads_per_cta(group);
   const long long items = static_cast<long long>(B) * Hkv * ((group + per - 1) / per);
-  // enough CTAs for four waves of four per SM (ragged lengths even out), of two blocks or more
-  const long long want = (16LL * 152 + items - 1) / items;
-  const long long most = (blocks + 1) / 2;
-  return static_cast<int>(want < 1 ? 1 : want < most ? want : most);
+  // a CTA's run of blocks with every sequence at its full length and some 456
+  // CTAs (three per SM); twice the pieces that makes, for ragged lengths
+  const long long run = (items * blocks + 455) / 456;
+  const long long want = 2 * ((blocks + run - 1) / run) + 1;
+  return static_cast<int>(items >= 4 * 456 ? 1 : want < blocks ? want : blocks);
 }
 
 extern "C" size_t attn_decode_cache_fp8_workspace_size(int B, int Hq, int d, int num_splits) {
-  return num_splits == 1 ? 256 : attn_decode_fp8_workspace_size(B, Hq, d, num_splits);
+  if (num_splits == 1 || B < 1 || Hq < 1) return 256;
+  return attn_decode_fp8_workspace_size(B, Hq, d, num_splits) + (static_cast<size_t>(B) * Hq * 4 + 255) / 256 * 256;
 }
 
 extern "C" attn_status attn_decode_cache_fp8(const void* q, const void* k8, const void* v8, const float* sk,
@@ -616,9 +777,8 @@ extern "C" attn_status attn_decode_cache_fp8(const void* q, const void* k8, cons
   a.group = Hq / Hkv;
   const int per = heads_per_cta(a.group);
   a.row_groups = (a.group + per - 1) / per;
-  a.blocks_per_split = (blocks + num_splits - 1) / num_splits;
-  a.splits = (blocks + a.blocks_per_split - 1) / a.blocks_per_split;   // those that hold a block
-  if (static_cast<long long>(B) * Hkv * a.row_groups * a.splits > INT_MAX) return ATTN_ERR_SHAPE;
+  a.splits = num_splits;
+  a.min_quota = num_splits > 1 ? (blocks + num_splits - 2) / (num_splits - 1) : 1;
   int* status;
   attn_status s = device_context(&status);
   if (s != ATTN_OK) return s;
@@ -635,6 +795,7 @@ extern "C" attn_status attn_decode_cache_fp8(const void* q, const void* k8, cons
   const size_t rows = static_cast<size_t>(num_splits) * B * Hq;
   a.o_part = static_cast<float*>(workspace);
   a.lse_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (rows * d * 4 + 255) / 256 * 256);
+  a.pieces = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(a.lse_part) + (rows * 4 + 255) / 256 * 256);
   a.B = B;
   a.Hq = Hq;
   a.Hkv = Hkv;

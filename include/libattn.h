@@ -372,13 +372,12 @@ ATTN_API attn_status attn_cache_append_fp8(const void* k, const void* v, const l
                                            int Nmax, int num_pages, int d, int rot_dim, int n_pos, int interleaved,
                                            attn_dtype dtype, void* stream);
 
-/* Splits that suit attn_decode_cache_fp8 for these sizes (blocks: ceil(Nmax /
- * 128)): enough CTAs to fill the GPU several times over. 0 for sizes out of
- * range. No device work. */
+/* A number of splits that suits attn_decode_cache_fp8 for these sizes
+ * (blocks: ceil(Nmax / 128)). 0 for sizes out of range. No device work. */
 ATTN_API int attn_decode_cache_fp8_splits(int B, int Hq, int Hkv, int blocks);
 
-/* Bytes of workspace attn_decode_cache_fp8 needs (that of attn_decode_fp8;
- * 256 for one split, which needs no partial results). */
+/* Bytes of workspace attn_decode_cache_fp8 needs: that of attn_decode_fp8 and
+ * 4 B Hq, rounded up to 256 (256 for one split, which has no partial results). */
 ATTN_API size_t attn_decode_cache_fp8_workspace_size(int B, int Hq, int d, int num_splits);
 
 /*
@@ -397,9 +396,10 @@ ATTN_API size_t attn_decode_cache_fp8_workspace_size(int B, int Hq, int d, int n
  * page is outside [0, num_pages) are not seen, and attn_get_device_status
  * then returns ATTN_ERR_SHAPE. What the cache holds outside the visible rows
  * (unwritten memory included) has no influence.
- * 1 <= num_splits <= ceil(Nmax/128): each split is a run of ceil(blocks /
- * num_splits) blocks from the first visible one; a second kernel combines
- * them. workspace: attn_decode_cache_fp8_workspace_size bytes; concurrent
+ * 1 <= num_splits <= ceil(Nmax/128): the pieces that a sequence's visible
+ * blocks may be cut into. The blocks of all sequences are dealt out evenly,
+ * whatever their lengths, and a second kernel combines the pieces; with one
+ * split a sequence's KV head is one CTA's work. workspace: attn_decode_cache_fp8_workspace_size bytes; concurrent
  * calls need workspaces of their own. score_cap negative, infinite or NaN:
  * ATTN_ERR_SHAPE.
  */
