@@ -45,6 +45,10 @@ struct AppendArgs {
   int* status;
 };
 
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ uint32_t max_u8x4(uint32_t a, uint32_t b) { return __vmaxu4(a, b); }
 
 // value of the E4M3 magnitude `m` (0 .. 126)
@@ -54,48 +58,67 @@ __device__ __forceinline__ float e4m3_magnitude(uint32_t m) {
                  : __uint_as_float(((ex + 120u) << 23) | (man << 20));          // 2^(ex-7) (1 + man/8)
 }
 
-// Element chunks of a row: 16 elements per thread. Rotated: 8 pairs (two
-// vectors, half apart or adjacent); past `rot`, 16 consecutive elements.
-template <typename T, int D>
-__device__ __forceinline__ void load_chunk(const AppendArgs& a, const T* row, int c, bool turn, int pos, int& e0,
-                                           int& e1, float (&v0)[8], float (&v1)[8]) {
-  const int half = a.rot / 2;
-  const bool split = turn && !a.interleaved;
-  e0 = split ? 8 * c : 16 * c;
-  e1 = split ? half + 8 * c : 16 * c + 8;
-  unpack8<T>(*reinterpret_cast<const uint4*>(row + e0), v0);
-  unpack8<T>(*reinterpret_cast<const uint4*>(row + e1), v1);
-  if (!turn) return;
-  const float* ct = a.cos + static_cast<long long>(pos) * half + 8 * c;
-  const float* st = a.sin + static_cast<long long>(pos) * half + 8 * c;
-  float cs[8], sn[8];
+// A row's chunks of 16 elements, one per thread, as floats in two arrays:
+// elements 0, 2, .. of the chunk's two vectors in v0 and 1, 3, .. in v1, or,
+// where the pairs are half the rotated part apart, the vectors themselves.
+// Either way a pair is (v0[i], v1[i]); every product and sum of its rotation is
+// rounded on its own.
+template <typename T>
+__device__ __forceinline__ void chunk_values(const AppendArgs& a, const uint4& w0, const uint4& w1, int c, bool turn,
+                                             bool apart, int pos, float2 (&v0)[4], float2 (&v1)[4]) {
+  if (apart) {
+    float f[8];
+    unpack8<T>(w0, f);
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const float4 u = __ldg(reinterpret_cast<const float4*>(ct) + q), w = __ldg(reinterpret_cast<const float4*>(st) + q);
-    cs[4 * q] = u.x; cs[4 * q + 1] = u.y; cs[4 * q + 2] = u.z; cs[4 * q + 3] = u.w;
-    sn[4 * q] = w.x; sn[4 * q + 1] = w.y; sn[4 * q + 2] = w.z; sn[4 * q + 3] = w.w;
-  }
-  auto turned = [](float& p, float& q, float c_, float s_) {
-    const float u = __fsub_rn(__fmul_rn(p, c_), __fmul_rn(q, s_));
-    q = __fadd_rn(__fmul_rn(q, c_), __fmul_rn(p, s_));
-    p = u;
-  };
-  if (a.interleaved) {
+    for (int i = 0; i < 4; ++i) v0[i] = make_float2(f[2 * i], f[2 * i + 1]);
+    unpack8<T>(w1, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v1[i] = make_float2(f[2 * i], f[2 * i + 1]);
+  } else {
+    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      turned(v0[2 * i], v0[2 * i + 1], cs[i], sn[i]);
-      turned(v1[2 * i], v1[2 * i + 1], cs[4 + i], sn[4 + i]);
+      v0[i] = make_float2(to_f32<T>(w[2 * i] & 0xFFFFu), to_f32<T>(w[2 * i + 1] & 0xFFFFu));
+      v1[i] = make_float2(to_f32<T>(w[2 * i] >> 16), to_f32<T>(w[2 * i + 1] >> 16));
     }
-  } else {
+  }
+  if (!turn) return;
+  const long long at = static_cast<long long>(pos) * (a.rot / 2) + 8 * c;
+  const float4* ct = reinterpret_cast<const float4*>(a.cos + at);
+  const float4* st = reinterpret_cast<const float4*>(a.sin + at);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) turned(v0[i], v1[i], cs[i], sn[i]);
+  for (int q = 0; q < 2; ++q) {
+    const float4 cs = __ldg(ct + q), sn = __ldg(st + q);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float2 c2 = u == 0 ? make_float2(cs.x, cs.y) : make_float2(cs.z, cs.w);
+      const float2 s2 = u == 0 ? make_float2(sn.x, sn.y) : make_float2(sn.z, sn.w);
+      const float2 p = v0[2 * q + u], r = v1[2 * q + u];
+      // the sums in scalar arithmetic: packed products and packed sums came out fused
+      const float2 pc = fmul2(p, c2), rs = fmul2(r, s2), rc = fmul2(r, c2), ps = fmul2(p, s2);
+      v0[2 * q + u] = make_float2(__fsub_rn(pc.x, rs.x), __fsub_rn(pc.y, rs.y));
+      v1[2 * q + u] = make_float2(__fadd_rn(rc.x, ps.x), __fadd_rn(rc.y, ps.y));
+    }
   }
 }
+// The larger of two packed pairs of 16-bit magnitudes (of finite values: they
+// order as integers).
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
 
+// The block's new rows go to shared memory first, all of them in flight
+// together whatever the registers (asynchronous 16-byte copies); they are
+// turned twice from there, for the largest magnitude and for the codes. (Held
+// in registers instead: 88 of them, 43 us for the prompt case; read from
+// memory twice: 36 us.)
 template <typename T, int D>
 __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
   constexpr int CH = D / 16;            // chunks per row
   constexpr int RSTEP = 256 / CH;       // rows per pass
+  extern __shared__ uint4 rows_smem[];  // [new rows][D / 8]
   __shared__ float red[8];
   const int h = blockIdx.y, b = static_cast<int>(blockIdx.z) >> 1, kv = blockIdx.z & 1;
   const int start = a.seqlens[b];
@@ -131,19 +154,38 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
   const bool turn = rope && 16 * c < a.rot;
   // largest magnitude of the rows that were there and of the new ones
   const float s_old = r0 > 0 ? a.scales[kv][si] : 1.f;
-  float amax = 0.f;
-  for (int r = r0 + rt; r < r1; r += RSTEP) {
-    int e0, e1;
-    float v0[8], v1[8];
-    load_chunk<T, D>(a, x + r * a.x_sn[kv], c, turn, blk * 128 + r, e0, e1, v0, v1);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmax3(amax, fabsf(v0[i]), fabsf(v1[i]));
-  }
+  constexpr int VPR = D / 8;            // vectors per row
+  for (int i = threadIdx.x; i < (r1 - r0) * VPR; i += 256)
+    copy_async16(rows_smem + i, x + (r0 + i / VPR) * a.x_sn[kv] + (i % VPR) * 8);
+  // vectors of this thread's chunk within a row
+  const bool apart = turn && !a.interleaved;
+  const int e0 = apart ? 8 * c : 16 * c, e1 = apart ? a.rot / 2 + 8 * c : 16 * c + 8;
   uint32_t held = 0;
   for (int i = threadIdx.x; i < r0 * (D / 16); i += 256) {
     const uint4 w = reinterpret_cast<const uint4*>(x8)[i];
     held = max_u8x4(held, max_u8x4(max_u8x4(w.x & 0x7f7f7f7fu, w.y & 0x7f7f7f7fu),
                                    max_u8x4(w.z & 0x7f7f7f7fu, w.w & 0x7f7f7f7fu)));
+  }
+  copy_async_wait();
+  __syncthreads();
+  float amax = 0.f;
+  if (turn) {
+    for (int r = rt; r < r1 - r0; r += RSTEP) {
+      float2 v0[4], v1[4];
+      chunk_values<T>(a, rows_smem[r * VPR + e0 / 8], rows_smem[r * VPR + e1 / 8], c, true, apart, blk * 128 + r0 + r, v0, v1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        amax = fmax3(fmax3(amax, fabsf(v0[i].x), fabsf(v0[i].y)), fabsf(v1[i].x), fabsf(v1[i].y));
+    }
+  } else {   // as they are: 16-bit magnitudes
+    uint32_t most = 0;
+    for (int r = rt; r < r1 - r0; r += RSTEP) {
+      const uint4 p = rows_smem[r * VPR + e0 / 8], q = rows_smem[r * VPR + e1 / 8];
+      const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) most = max_u16x2(most, w[i] & 0x7fff7fffu);
+    }
+    amax = fmaxf(to_f32<T>(most & 0xFFFFu), to_f32<T>(most >> 16));
   }
   uint32_t m = max(max(held & 0xffu, (held >> 8) & 0xffu), max((held >> 16) & 0xffu, held >> 24));
   amax = fmaxf(amax, e4m3_magnitude(min(m, 126u)) * s_old);   // a NaN code (127) counts as 448
@@ -155,8 +197,9 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
 #pragma unroll
   for (int i = 1; i < 8; ++i) amax = fmaxf(amax, red[i]);
   const int e = e4m3_scale_exponent(amax);
-  // 2^e in two factors, both normal floats whatever e is
-  const float f1 = ldexpf(1.f, e / 2), f2 = ldexpf(1.f, e - e / 2);
+  // 2^e in one factor if it is a normal float, else in two
+  const int ea = e >= -126 && e <= 127 ? e : e / 2;
+  const float f1 = ldexpf(1.f, ea), f2 = ldexpf(1.f, e - ea);
   const float s_new = ldexpf(1.f, -e);
   if (threadIdx.x == 0) a.scales[kv][si] = s_new;
   if (r0 > 0 && s_new != s_old) {   // the earlier rows at the new factor
@@ -177,21 +220,53 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
       reinterpret_cast<uint4*>(x8)[i] = w;
     }
   }
-  for (int r = r0 + rt; r < r1; r += RSTEP) {
-    int e0, e1;
-    float v0[8], v1[8];
-    load_chunk<T, D>(a, x + r * a.x_sn[kv], c, turn, blk * 128 + r, e0, e1, v0, v1);
+  for (int r = rt; r < r1 - r0; r += RSTEP) {
+    float2 v0[4], v1[4];
+    chunk_values<T>(a, rows_smem[r * VPR + e0 / 8], rows_smem[r * VPR + e1 / 8], c, turn, apart, blk * 128 + r0 + r, v0, v1);
+    const float2 g = make_float2(f1, f1);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v0[i] = v0[i] * f1 * f2;
-      v1[i] = v1[i] * f1 * f2;
+    for (int i = 0; i < 4; ++i) {
+      v0[i] = fmul2(v0[i], g);
+      v1[i] = fmul2(v1[i], g);
     }
-    uint8_t* dst = x8 + r * D;
-    *reinterpret_cast<uint2*>(dst + e0) = make_uint2(pack_e4m3x4(v0[0], v0[1], v0[2], v0[3]),
-                                                     pack_e4m3x4(v0[4], v0[5], v0[6], v0[7]));
-    *reinterpret_cast<uint2*>(dst + e1) = make_uint2(pack_e4m3x4(v1[0], v1[1], v1[2], v1[3]),
-                                                     pack_e4m3x4(v1[4], v1[5], v1[6], v1[7]));
+    if (f2 != 1.f) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v0[i] = fmul2(v0[i], make_float2(f2, f2));
+        v1[i] = fmul2(v1[i], make_float2(f2, f2));
+      }
+    }
+    uint32_t o0[2], o1[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 p = v0[2 * i], q = v0[2 * i + 1], y = v1[2 * i], z = v1[2 * i + 1];
+      if (apart) {
+        o0[i] = pack_e4m3x4(p.x, p.y, q.x, q.y);
+        o1[i] = pack_e4m3x4(y.x, y.y, z.x, z.y);
+      } else {   // elements 8i .. 8i + 7 of the chunk
+        o0[i] = pack_e4m3x4(p.x, y.x, p.y, y.y);
+        o1[i] = pack_e4m3x4(q.x, z.x, q.y, z.y);
+      }
+    }
+    uint8_t* dst = x8 + (r0 + r) * D;
+    if (apart) {
+      *reinterpret_cast<uint2*>(dst + e0) = make_uint2(o0[0], o0[1]);
+      *reinterpret_cast<uint2*>(dst + e1) = make_uint2(o1[0], o1[1]);
+    } else {
+      *reinterpret_cast<uint4*>(dst + e0) = make_uint4(o0[0], o1[0], o0[1], o1[1]);
+    }
   }
+}
+
+template <typename T, int D>
+cudaError_t launch_append_dim(const AppendArgs& a, dim3 grid, cudaStream_t st) {
+  const int bytes = (a.n_new < 128 ? a.n_new : 128) * D * 2;   // most new rows of a block
+  if (bytes > 48 * 1024) {
+    const cudaError_t e = smem_attr_once<append_kernel<T, D>>(128 * D * 2);
+    if (e != cudaSuccess) return e;
+  }
+  append_kernel<T, D><<<grid, 256, bytes, st>>>(a);
+  return cudaGetLastError();
 }
 
 template <typename T>
@@ -199,11 +274,10 @@ cudaError_t launch_append(int d, const AppendArgs& a, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>((a.n_new + 126) / 128 + 1), static_cast<unsigned>(a.Hkv),
                   static_cast<unsigned>(2 * a.B));
   switch (d) {
-    case 64: append_kernel<T, 64><<<grid, 256, 0, st>>>(a); break;
-    case 128: append_kernel<T, 128><<<grid, 256, 0, st>>>(a); break;
-    default: append_kernel<T, 256><<<grid, 256, 0, st>>>(a); break;
+    case 64: return launch_append_dim<T, 64>(a, grid, st);
+    case 128: return launch_append_dim<T, 128>(a, grid, st);
+    default: return launch_append_dim<T, 256>(a, grid, st);
   }
-  return cudaGetLastError();
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -126,9 +126,13 @@ __device__ __forceinline__ float cap_score(float x, float cap_log2) {
   return cap_log2 - 2.f * cap_log2 * rcp_approx(1.f + ex2(x));
 }
 
+// Keys per tile of a warp, in sixteens: 64 registers of K and V (128 bytes a
+// lane in flight), fewer where O and Q already fill them.
+template <int D, int NR>
+__host__ __device__ constexpr int decode_groups() { return D == 256 ? 1 : D == 64 ? 4 / NR : 2 / NR; }
 // CTAs per SM the kernel is built for.
 template <int D, int NR>
-constexpr int decode_ctas() { return D == 256 ? 2 : NR == 2 ? 3 : 4; }
+constexpr int decode_ctas() { return D == 256 ? 2 : 3; }
 
 // Visible keys [x, y) of a sequence.
 __device__ __forceinline__ int2 visible_keys(const CacheDecArgs& a, int b) {
@@ -205,70 +209,80 @@ __device__ __forceinline__ void decode_piece(const CacheDecArgs& a, float* smem,
   };
   load_set(blk0);
 
-  // The walk: units of 64 keys (half a block), every fourth one this warp's,
-  // in tiles of 16. All of it is the same in every lane.
-  const int unit_end = min(blk1 * 2, (L + 63) >> 6);
-  int unit = max(blk0 * 2, lo >> 6) + warp - kWarps, sub = 0, sub_end = 0;
-  float sk_u = 1.f, sv_u = 1.f;   // the unit's factors
+  // The walk: units of one tile of KEYS keys (two of the smallest), every
+  // fourth one this warp's. All of it is the same in every lane.
+  constexpr int KT = decode_groups<D, NR>(), KEYS = 16 * KT, SUB = KT == 1 ? 2 : 1, UNIT = KEYS * SUB;
+  const int unit_end = min(blk1 * (128 / UNIT), (L + UNIT - 1) / UNIT);
+  int unit = max(blk0 * (128 / UNIT), lo / UNIT) + warp - kWarps;
+  int key0 = 0;                   // the tile's first key
+  float sk_t = 1.f, sv_t = 1.f;   // the tile's factors
   const uint8_t *kp = a.k8, *vp = a.v8;   // this lane's first bytes of the tile
-  auto advance = [&]() -> bool {   // to the next tile; false past the last one
-    ++sub;
-    kp += 16 * D;
-    vp += 16 * D;
-    while (sub >= sub_end) {
+  bool second = false;            // the unit's other tile is to come
+  auto advance = [&]() -> bool {  // to the next tile; false past the last one
+    if (SUB == 2 && second) {
+      second = false;
+      key0 += KEYS;
+      kp += KEYS * D;
+      vp += KEYS * D;
+      return true;
+    }
+    while (true) {
       unit += kWarps;
       if (unit >= unit_end) return false;
-      const int blk = unit >> 1;
+      const int blk = unit / (128 / UNIT);
       if (blk >= set0 + 32) load_set(blk);
       const int page = __shfl_sync(0xffffffffu, page_l, blk - set0);
-      sk_u = __shfl_sync(0xffffffffu, sk_l, blk - set0);
-      sv_u = __shfl_sync(0xffffffffu, sv_l, blk - set0);
-      if (page < 0) continue;   // (sub_end is still reached)
-      sub = max(lo - unit * 64, 0) >> 4;
-      sub_end = (min(L - unit * 64, 64) + 15) >> 4;
+      sk_t = __shfl_sync(0xffffffffu, sk_l, blk - set0);
+      sv_t = __shfl_sync(0xffffffffu, sv_l, blk - set0);
+      if (page < 0) continue;
       const long long row = (a.table ? (static_cast<long long>(page) * a.Hkv + h) * 128
                                      : (static_cast<long long>(b) * a.Hkv + h) * a.rows_max +
-                                           static_cast<long long>(blk) * 128) + (unit & 1) * 64 + sub * 16;
+                                           static_cast<long long>(blk) * 128) + (unit % (128 / UNIT)) * UNIT;
+      key0 = unit * UNIT;
       kp = a.k8 + (row + g) * D + 16 * t;
       vp = a.v8 + (row + 2 * t) * D + VB * g;
+      second = SUB == 2 && key0 + KEYS < L;
+      return true;
     }
-    return true;
   };
-  // K and V of the tile's 16 keys; in a tile that is cut, rows that are not
+  // K and V of the tile's keys; in a tile that is cut, rows that are not
   // visible stay zero, whatever the cache holds there
-  uint32_t kr[2][NG][4];          // keys g, g + 8
-  uint32_t vr[4][NH][VB / 4];     // keys 2t, 2t + 1, 2t + 8, 2t + 9
+  uint32_t kr[KT][2][NG][4];          // of each 16 keys g, g + 8
+  uint32_t vr[KT][4][NH][VB / 4];     // keys 2t, 2t + 1, 2t + 8, 2t + 9
   auto load_k = [&](int key0, bool cut) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int key = key0 + g + 8 * r;
-      const bool in = !cut || (key >= lo && key < L);
+    for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int c = 0; c < NG; ++c) {
-        if (in) load_bytes<16>(kr[r][c], kp + r * 8 * D + 64 * c);
-        else kr[r][c][0] = kr[r][c][1] = kr[r][c][2] = kr[r][c][3] = 0;
+      for (int r = 0; r < 2; ++r) {
+        const int key = key0 + 16 * kt + g + 8 * r;
+        const bool in = !cut || (key >= lo && key < L);
+#pragma unroll
+        for (int c = 0; c < NG; ++c) {
+          if (in) load_bytes<16>(kr[kt][r][c], kp + (16 * kt + 8 * r) * D + 64 * c);
+          else kr[kt][r][c][0] = kr[kt][r][c][1] = kr[kt][r][c][2] = kr[kt][r][c][3] = 0;
+        }
       }
-    }
   };
   auto load_v = [&](int key0, bool cut) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = (r & 1) + 8 * (r >> 1), key = key0 + 2 * t + row;
-      const bool in = !cut || (key >= lo && key < L);
+    for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int c = 0; c < NH; ++c) {
-        if (in) {
-          load_bytes<VB>(vr[r][c], vp + row * D + 128 * c);
-        } else {
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * kt + (r & 1) + 8 * (r >> 1), key = key0 + 2 * t + row;
+        const bool in = !cut || (key >= lo && key < L);
 #pragma unroll
-          for (int i = 0; i < VB / 4; ++i) vr[r][c][i] = 0;
+        for (int c = 0; c < NH; ++c) {
+          if (in) {
+            load_bytes<VB>(vr[kt][r][c], vp + row * D + 128 * c);
+          } else {
+#pragma unroll
+            for (int i = 0; i < VB / 4; ++i) vr[kt][r][c][i] = 0;
+          }
         }
       }
-    }
   };
   bool more = advance();
-  int key0 = unit * 64 + sub * 16;   // the tile's first key
-  bool cut = key0 < lo || key0 + 16 > L;
+  bool cut = key0 < lo || key0 + KEYS > L;
   if (more) {
     if (cut) {
       load_k(key0, true);
@@ -337,52 +351,57 @@ __device__ __forceinline__ void decode_piece(const CacheDecArgs& a, float* smem,
   float s_cur = 0.f;              // O is held in units of this factor (0: none yet)
 
   while (more) {
-    const float sk = sk_u, sv = sv_u;
-    const int key = key0 + g;
+    const float sk = sk_t, sv = sv_t;
+    const int key = key0 + g;     // (advance() below moves key0)
     const bool edge = cut;
-    float s[NR][4];
+    float s[NR][KT][4];
 #pragma unroll
-    for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
-    for (int c = 0; c < NG; ++c)
+      for (int kt = 0; kt < KT; ++kt) s[n][kt][0] = s[n][kt][1] = s[n][kt][2] = s[n][kt][3] = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t a0 = e4m3x2_to_f16x2(kr[0][c][w]), a2 = e4m3x2_to_f16x2(kr[0][c][w] >> 16);
-        const uint32_t a1 = e4m3x2_to_f16x2(kr[1][c][w]), a3 = e4m3x2_to_f16x2(kr[1][c][w] >> 16);
+    for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-        for (int n = 0; n < NR; ++n) mma_16816(s[n], a0, a1, a2, a3, qf[n][c][w][0], qf[n][c][w][1]);
-      }
+      for (int c = 0; c < NG; ++c)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t k0 = kr[kt][0][c][w], k1 = kr[kt][1][c][w];
+          const uint32_t a0 = e4m3x2_to_f16x2(k0), a2 = e4m3x2_to_f16x2(k0 >> 16);
+          const uint32_t a1 = e4m3x2_to_f16x2(k1), a3 = e4m3x2_to_f16x2(k1 >> 16);
+#pragma unroll
+          for (int n = 0; n < NR; ++n) mma_16816(s[n][kt], a0, a1, a2, a3, qf[n][c][w][0], qf[n][c][w][1]);
+        }
     more = advance();   // the next tile's loads go out as the registers come free
-    key0 = unit * 64 + sub * 16;
-    cut = key0 < lo || key0 + 16 > L;
+    cut = key0 < lo || key0 + KEYS > L;
     if (more) {
       if (cut) load_k(key0, true);
       else load_k(key0, false);
     }
-    // scores in log2 units: values 0, 1 are key g, values 2, 3 key g + 8, of heads 2t and 2t + 1
-#pragma unroll
-    for (int n = 0; n < NR; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x = s[n][e] * (qscale[n][e & 1] * sk);
-        if (a.cap > 0.f) x = cap_score(x, a.cap_log2);
-        const int at = key + 8 * (e >> 1);
-        if (a.slopes) x -= slope2[n][e & 1] * static_cast<float>(L - 1 - at);
-        if (edge && (at < lo || at >= L)) x = -INFINITY;
-        s[n][e] = x;
-      }
-    // move the running max where a score passes it by more than kTau
+    // scores in log2 units: of each 16 keys values 0, 1 are key g, values 2, 3 key g + 8, of heads 2t and 2t + 1
     bool up = false;
 #pragma unroll
     for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) up |= fmaxf(s[n][u], s[n][2 + u]) > m[n][u] + kTau;
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = s[n][kt][e] * (qscale[n][e & 1] * sk);
+          if (a.cap > 0.f) x = cap_score(x, a.cap_log2);
+          const int at = key + 16 * kt + 8 * (e >> 1);
+          if (a.slopes) x -= slope2[n][e & 1] * static_cast<float>(L - 1 - at);
+          if (edge && (at < lo || at >= L)) x = -INFINITY;
+          s[n][kt][e] = x;
+          up |= x > m[n][e & 1] + kTau;
+        }
+    // move the running max where a score passes it by more than kTau
     if (warp_any(up)) {
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          float mx = fmaxf(s[n][u], s[n][2 + u]);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt) mx = fmax3(mx, s[n][kt][u], s[n][kt][2 + u]);
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -410,34 +429,41 @@ __device__ __forceinline__ void decode_piece(const CacheDecArgs& a, float* smem,
       }
       s_cur = sv;
     }
-    uint32_t pb[NR][2];
+    uint32_t pb[NR][KT][2];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       const float mu0 = (m[n][0] == -INFINITY ? 0.f : m[n][0]) - kPShift;
       const float mu1 = (m[n][1] == -INFINITY ? 0.f : m[n][1]) - kPShift;
-      const float p0 = ex2(s[n][0] - mu0), p1 = ex2(s[n][1] - mu1), p2 = ex2(s[n][2] - mu0), p3 = ex2(s[n][3] - mu1);
-      l[n][0] += p0 + p2;
-      l[n][1] += p1 + p3;
-      pb[n][0] = transpose_8x8(pack_f16x2(p0, p1));
-      pb[n][1] = transpose_8x8(pack_f16x2(p2, p3));
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        const float(&x)[4] = s[n][kt];
+        const float p0 = ex2(x[0] - mu0), p1 = ex2(x[1] - mu1), p2 = ex2(x[2] - mu0), p3 = ex2(x[3] - mu1);
+        l[n][0] += p0 + p2;
+        l[n][1] += p1 + p3;
+        pb[n][kt][0] = transpose_8x8(pack_f16x2(p0, p1));
+        pb[n][kt][1] = transpose_8x8(pack_f16x2(p2, p3));
+      }
     }
 #pragma unroll
-    for (int c = 0; c < NH; ++c)
+    for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int w = 0; w < VB / 4; ++w) {
-        const uint32_t k01a = __byte_perm(vr[0][c][w], vr[1][c][w], 0x5140), k01b = __byte_perm(vr[0][c][w], vr[1][c][w], 0x7362);
-        const uint32_t k89a = __byte_perm(vr[2][c][w], vr[3][c][w], 0x5140), k89b = __byte_perm(vr[2][c][w], vr[3][c][w], 0x7362);
-        const int i = c * (VB / 2) + 2 * w;
-        const uint32_t a0 = e4m3x2_to_f16x2(k01a), a1 = e4m3x2_to_f16x2(k01a >> 16);
-        const uint32_t a2 = e4m3x2_to_f16x2(k89a), a3 = e4m3x2_to_f16x2(k89a >> 16);
-        const uint32_t b0 = e4m3x2_to_f16x2(k01b), b1 = e4m3x2_to_f16x2(k01b >> 16);
-        const uint32_t b2 = e4m3x2_to_f16x2(k89b), b3 = e4m3x2_to_f16x2(k89b >> 16);
+      for (int c = 0; c < NH; ++c)
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
-          mma_16816(acc[n][i], a0, a1, a2, a3, pb[n][0], pb[n][1]);
-          mma_16816(acc[n][i + 1], b0, b1, b2, b3, pb[n][0], pb[n][1]);
+        for (int w = 0; w < VB / 4; ++w) {
+          const uint32_t v0 = vr[kt][0][c][w], v1 = vr[kt][1][c][w], v2 = vr[kt][2][c][w], v3 = vr[kt][3][c][w];
+          const uint32_t k01a = __byte_perm(v0, v1, 0x5140), k01b = __byte_perm(v0, v1, 0x7362);
+          const uint32_t k89a = __byte_perm(v2, v3, 0x5140), k89b = __byte_perm(v2, v3, 0x7362);
+          const int i = c * (VB / 2) + 2 * w;
+          const uint32_t a0 = e4m3x2_to_f16x2(k01a), a1 = e4m3x2_to_f16x2(k01a >> 16);
+          const uint32_t a2 = e4m3x2_to_f16x2(k89a), a3 = e4m3x2_to_f16x2(k89a >> 16);
+          const uint32_t b0 = e4m3x2_to_f16x2(k01b), b1 = e4m3x2_to_f16x2(k01b >> 16);
+          const uint32_t b2 = e4m3x2_to_f16x2(k89b), b3 = e4m3x2_to_f16x2(k89b >> 16);
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            mma_16816(acc[n][i], a0, a1, a2, a3, pb[n][kt][0], pb[n][kt][1]);
+            mma_16816(acc[n][i + 1], b0, b1, b2, b3, pb[n][kt][0], pb[n][kt][1]);
+          }
         }
-      }
     if (more) {
       if (cut) load_v(key0, true);
       else load_v(key0, false);
@@ -631,54 +657,81 @@ decode_cache_kernel(const CacheDecArgs a) {
   }
 }
 
-// One warp per (sequence, query head), D / 32 head dims per lane. Lane i has
-// split i's log-sum-exp (of each 32), so the splits' partial rows can be
-// loaded one behind the other without waiting.
-template <typename T, int D, int NR>
-__global__ void __launch_bounds__(128) combine_kernel(const CacheDecArgs a) {
+// kSplit warps per (sequence, query head), each with every kSplit-th piece,
+// D / 32 head dims per lane. Lane i has the log-sum-exp of piece i of 32, so
+// the pieces' rows can be loaded one behind the other without waiting; many
+// pieces of few rows (a long cache of one sequence) take eight warps a row
+// (74 pieces of 32 rows: 42 us with one).
+template <typename T, int D, int NR, int kSplit>
+__global__ void __launch_bounds__(256) combine_kernel(const CacheDecArgs a) {
   constexpr int N = D / 32, V = N < 4 ? N : 4;
+  __shared__ float part[kSplit > 1 ? 8 : 1][D];
+  __shared__ float part_tot[8];
   const int rows = a.B * a.Hq;
-  const int r = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const float* __restrict__ o_part = a.o_part;
-  const float* __restrict__ lse_part = a.lse_part;
-  int splits = 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.x * (8 / kSplit) + warp / kSplit, sub = warp % kSplit;
   const int b = r < rows ? r / a.Hq : 0, hq = r - b * a.Hq, h = hq / a.group;
   const int item = (b * a.Hkv + h) * a.row_groups + (hq - h * a.group) / (8 * NR);
   grid_wait_prerequisites();   // launched while the pieces' kernel runs
   if (r >= rows) return;
+  int pieces = 0;
   if (a.seqlens[b] > 0) {
-    splits = a.pieces[item];
-    if (splits == 1) return;   // written already
+    pieces = a.pieces[item];
+    if (pieces == 1) return;   // written already (with kSplit = 8 the whole CTA leaves)
   }
+  const float* lse_part = a.lse_part + r;
+  const float* o_part = a.o_part + static_cast<long long>(r) * D + lane * V;
   float mx = -INFINITY;
-  for (int s = lane; s < splits; s += 32) mx = fmaxf(mx, lse_part[static_cast<long long>(s) * rows + r]);
+  for (int s = lane; s < pieces; s += 32) mx = fmaxf(mx, lse_part[static_cast<long long>(s) * rows]);
 #pragma unroll
   for (int i = 16; i > 0; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
   float tot = 0.f, x[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = 0.f;
-  for (int s0 = 0; s0 < splits; s0 += 32) {
-    const float z = s0 + lane < splits ? lse_part[static_cast<long long>(s0 + lane) * rows + r] : -INFINITY;
+  for (int s0 = sub; s0 < pieces; s0 += 32 * kSplit) {   // lane i: piece s0 + i kSplit
+    const int mine = s0 + lane * kSplit;
+    const float z = mine < pieces ? lse_part[static_cast<long long>(mine) * rows] : -INFINITY;
     const float w_l = z == -INFINITY ? 0.f : expf(z - mx);
     tot += w_l;
-    const int n = min(32, splits - s0);
-#pragma unroll 4
-    for (int s = 0; s < n; ++s) {
-      const float w = __shfl_sync(0xffffffffu, w_l, s);
-      if (w == 0.f) continue;   // nothing seen (its O was not written), or nothing that counts
-      const float* src = o_part + (static_cast<long long>(s0 + s) * rows + r) * D + lane * V;
+    const int n = min(32, (pieces - s0 + kSplit - 1) / kSplit);
+    for (int s = 0; s < n; s += 4) {
+      float w[4], v[4][N];
 #pragma unroll
-      for (int c = 0; c < N / V; ++c) {
-        float v[V];
-        if constexpr (V == 4) *reinterpret_cast<float4*>(v) = __ldcs(reinterpret_cast<const float4*>(src + 128 * c));
-        else *reinterpret_cast<float2*>(v) = __ldcs(reinterpret_cast<const float2*>(src));
+      for (int u = 0; u < 4; ++u) {
+        w[u] = __shfl_sync(0xffffffffu, w_l, (s + u) & 31);
+        if (s + u >= n) w[u] = 0.f;
+        const float* src = o_part + static_cast<long long>(s0 + (s + u) * kSplit) * rows * D;
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[c * V + i] = fmaf(w, v[i], x[c * V + i]);
+        for (int c = 0; c < N / V; ++c) {
+          // a piece of weight 0 saw nothing (and wrote no O), or counts for nothing
+          if constexpr (V == 4)
+            *reinterpret_cast<float4*>(&v[u][4 * c]) =
+                w[u] != 0.f ? __ldcs(reinterpret_cast<const float4*>(src + 128 * c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          else
+            *reinterpret_cast<float2*>(&v[u][0]) =
+                w[u] != 0.f ? __ldcs(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
+        }
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = fmaf(w[u], v[u][i], x[i]);
     }
   }
 #pragma unroll
   for (int i = 16; i > 0; i >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, i);
+  if constexpr (kSplit > 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) part[warp][lane * V + (i / V) * 128 + i % V] = x[i];
+    if (lane == 0) part_tot[warp] = tot;
+    __syncthreads();
+    if (warp != 0) return;
+    for (int w = 1; w < kSplit; ++w) {
+      tot += part_tot[w];
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] += part[w][lane * V + (i / V) * 128 + i % V];
+    }
+  }
   const float inv = tot > 0.f ? 1.f / tot : 0.f;
   T* dst = static_cast<T*>(a.o) + static_cast<long long>(r) * D + lane * V;
 #pragma unroll
@@ -707,15 +760,18 @@ cudaError_t launch_decode(const CacheDecArgs& a, cudaStream_t st) {
   if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
   // a programmatic dependent: its launch overlaps the pieces' kernel, whose results it waits for
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.B * a.Hq + 3) / 4));
-  cfg.blockDim = dim3(128);
+  const long long rows = static_cast<long long>(a.B) * a.Hq;
+  const bool few = rows <= 4 * sms;   // eight warps a row still fit at once
+  cfg.gridDim = dim3(static_cast<unsigned>(few ? rows : (rows + 7) / 8));
+  cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<T, D, NR>, a);
+  return few ? cudaLaunchKernelEx(&cfg, combine_kernel<T, D, NR, 8>, a)
+             : cudaLaunchKernelEx(&cfg, combine_kernel<T, D, NR, 1>, a);
 }
 
 template <typename T>

