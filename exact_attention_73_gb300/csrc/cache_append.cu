@@ -58,14 +58,30 @@ __device__ __forceinline__ float e4m3_magnitude(uint32_t m) {
                  : __uint_as_float(((ex + 120u) << 23) | (man << 20));          // 2^(ex-7) (1 + man/8)
 }
 
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+// e4m3_scale_exponent from the bits: largest e with amax 2^e <= 448 (0 for 0)
+__device__ __forceinline__ int scale_exponent(float amax) {
+  if (!(amax > 0.f)) return 0;
+  int below = 0;
+  if (amax < 1.1754943508222875e-38f) {   // subnormal
+    amax *= 18446744073709551616.f;
+    below = 64;
+  }
+  const int bits = __float_as_int(amax);
+  // amax = m 2^k, m in [0.5, 1), m <= 0.875 in the leading mantissa bits
+  return ((bits & 0x7fffff) <= 0x600000 ? 9 : 8) - ((bits >> 23) - 126) + below;
+}
+
 // A row's chunks of 16 elements, one per thread, as floats in two arrays:
 // elements 0, 2, .. of the chunk's two vectors in v0 and 1, 3, .. in v1, or,
 // where the pairs are half the rotated part apart, the vectors themselves.
 // Either way a pair is (v0[i], v1[i]); every product and sum of its rotation is
 // rounded on its own.
 template <typename T>
-__device__ __forceinline__ void chunk_values(const AppendArgs& a, const uint4& w0, const uint4& w1, int c, bool turn,
-                                             bool apart, int pos, float2 (&v0)[4], float2 (&v1)[4]) {
+__device__ __forceinline__ void chunk_values(const uint4& w0, const uint4& w1, bool turn,
+                                             bool apart, const float* cos, const float* sin, float2 (&v0)[4],
+                                             float2 (&v1)[4]) {
   if (apart) {
     float f[8];
     unpack8<T>(w0, f);
@@ -83,9 +99,8 @@ __device__ __forceinline__ void chunk_values(const AppendArgs& a, const uint4& w
     }
   }
   if (!turn) return;
-  const long long at = static_cast<long long>(pos) * (a.rot / 2) + 8 * c;
-  const float4* ct = reinterpret_cast<const float4*>(a.cos + at);
-  const float4* st = reinterpret_cast<const float4*>(a.sin + at);
+  const float4* ct = reinterpret_cast<const float4*>(cos);
+  const float4* st = reinterpret_cast<const float4*>(sin);
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const float4 cs = __ldg(ct + q), sn = __ldg(st + q);
@@ -114,12 +129,15 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t x, uint32_t y) {
 // turned twice from there, for the largest magnitude and for the codes. (Held
 // in registers instead: 88 of them, 43 us for the prompt case; read from
 // memory twice: 36 us.)
+constexpr int kThreads = 128;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
   constexpr int CH = D / 16;            // chunks per row
-  constexpr int RSTEP = 256 / CH;       // rows per pass
+  constexpr int RSTEP = kThreads / CH;  // rows per pass
+  constexpr int NW = kThreads / 32;
   extern __shared__ uint4 rows_smem[];  // [new rows][D / 8]
-  __shared__ float red[8];
+  __shared__ float red[NW];
   const int h = blockIdx.y, b = static_cast<int>(blockIdx.z) >> 1, kv = blockIdx.z & 1;
   const int start = a.seqlens[b];
   int n = a.new_lens ? min(a.new_lens[b], a.n_new) : a.n_new;
@@ -155,35 +173,50 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
   // largest magnitude of the rows that were there and of the new ones
   const float s_old = r0 > 0 ? a.scales[kv][si] : 1.f;
   constexpr int VPR = D / 8;            // vectors per row
-  for (int i = threadIdx.x; i < (r1 - r0) * VPR; i += 256)
-    copy_async16(rows_smem + i, x + (r0 + i / VPR) * a.x_sn[kv] + (i % VPR) * 8);
+  {
+    const int row = threadIdx.x / VPR;
+    const T* src = x + (r0 + row) * a.x_sn[kv] + (threadIdx.x % VPR) * 8;
+    const long long step = (kThreads / VPR) * a.x_sn[kv];
+#pragma unroll 4
+    for (int i = threadIdx.x; i < (r1 - r0) * VPR; i += kThreads, src += step) copy_async16(rows_smem + i, src);
+  }
   // vectors of this thread's chunk within a row
   const bool apart = turn && !a.interleaved;
   const int e0 = apart ? 8 * c : 16 * c, e1 = apart ? a.rot / 2 + 8 * c : 16 * c + 8;
   uint32_t held = 0;
-  for (int i = threadIdx.x; i < r0 * (D / 16); i += 256) {
+  for (int i = threadIdx.x; i < r0 * (D / 16); i += kThreads) {
     const uint4 w = reinterpret_cast<const uint4*>(x8)[i];
     held = max_u8x4(held, max_u8x4(max_u8x4(w.x & 0x7f7f7f7fu, w.y & 0x7f7f7f7fu),
                                    max_u8x4(w.z & 0x7f7f7f7fu, w.w & 0x7f7f7f7fu)));
   }
   copy_async_wait();
   __syncthreads();
+  // this thread's rows: rt, rt + RSTEP, ... of the new ones
+  const uint4* in0 = rows_smem + rt * VPR + e0 / 8;
+  const uint4* in1 = rows_smem + rt * VPR + e1 / 8;
+  const int half = a.rot / 2, nr = r1 - r0;
+  const long long t0 = static_cast<long long>(blk * 128 + r0 + rt) * half + 8 * c;
+  const float* ct = a.cos + t0;
+  const float* st = a.sin + t0;
   float amax = 0.f;
   if (turn) {
-    for (int r = rt; r < r1 - r0; r += RSTEP) {
+#pragma unroll 2
+    for (int r = rt, i = 0; r < nr; r += RSTEP, ++i) {
       float2 v0[4], v1[4];
-      chunk_values<T>(a, rows_smem[r * VPR + e0 / 8], rows_smem[r * VPR + e1 / 8], c, true, apart, blk * 128 + r0 + r, v0, v1);
+      chunk_values<T>(in0[i * RSTEP * VPR], in1[i * RSTEP * VPR], true, apart, ct + i * RSTEP * half, st + i * RSTEP * half,
+                      v0, v1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        amax = fmax3(fmax3(amax, fabsf(v0[i].x), fabsf(v0[i].y)), fabsf(v1[i].x), fabsf(v1[i].y));
+      for (int k = 0; k < 4; ++k)
+        amax = fmax3(fmax3(amax, fabsf(v0[k].x), fabsf(v0[k].y)), fabsf(v1[k].x), fabsf(v1[k].y));
     }
   } else {   // as they are: 16-bit magnitudes
     uint32_t most = 0;
-    for (int r = rt; r < r1 - r0; r += RSTEP) {
-      const uint4 p = rows_smem[r * VPR + e0 / 8], q = rows_smem[r * VPR + e1 / 8];
+#pragma unroll 2
+    for (int r = rt, i = 0; r < nr; r += RSTEP, ++i) {
+      const uint4 p = in0[i * RSTEP * VPR], q = in1[i * RSTEP * VPR];
       const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) most = max_u16x2(most, w[i] & 0x7fff7fffu);
+      for (int k = 0; k < 8; ++k) most = max_u16x2(most, w[k] & 0x7fff7fffu);
     }
     amax = fmaxf(to_f32<T>(most & 0xFFFFu), to_f32<T>(most >> 16));
   }
@@ -195,15 +228,15 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
   __syncthreads();
   amax = red[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) amax = fmaxf(amax, red[i]);
-  const int e = e4m3_scale_exponent(amax);
+  for (int i = 1; i < NW; ++i) amax = fmaxf(amax, red[i]);
+  const int e = scale_exponent(amax);
   // 2^e in one factor if it is a normal float, else in two
   const int ea = e >= -126 && e <= 127 ? e : e / 2;
-  const float f1 = ldexpf(1.f, ea), f2 = ldexpf(1.f, e - ea);
-  const float s_new = ldexpf(1.f, -e);
+  const float f1 = pow2i(ea), f2 = pow2i(e - ea);
+  const float s_new = pow2i(-e / 2) * pow2i(-e - -e / 2);
   if (threadIdx.x == 0) a.scales[kv][si] = s_new;
   if (r0 > 0 && s_new != s_old) {   // the earlier rows at the new factor
-    for (int i = threadIdx.x; i < r0 * (D / 16); i += 256) {
+    for (int i = threadIdx.x; i < r0 * (D / 16); i += kThreads) {
       uint4 w = reinterpret_cast<const uint4*>(x8)[i];
       uint32_t* p = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
@@ -220,35 +253,38 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
       reinterpret_cast<uint4*>(x8)[i] = w;
     }
   }
-  for (int r = rt; r < r1 - r0; r += RSTEP) {
+  uint8_t* out = x8 + (r0 + rt) * D;
+#pragma unroll 2
+  for (int r = rt, i = 0; r < nr; r += RSTEP, ++i) {
     float2 v0[4], v1[4];
-    chunk_values<T>(a, rows_smem[r * VPR + e0 / 8], rows_smem[r * VPR + e1 / 8], c, turn, apart, blk * 128 + r0 + r, v0, v1);
+    chunk_values<T>(in0[i * RSTEP * VPR], in1[i * RSTEP * VPR], turn, apart, ct + i * RSTEP * half, st + i * RSTEP * half, v0,
+                    v1);
     const float2 g = make_float2(f1, f1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v0[i] = fmul2(v0[i], g);
-      v1[i] = fmul2(v1[i], g);
+    for (int k = 0; k < 4; ++k) {
+      v0[k] = fmul2(v0[k], g);
+      v1[k] = fmul2(v1[k], g);
     }
     if (f2 != 1.f) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v0[i] = fmul2(v0[i], make_float2(f2, f2));
-        v1[i] = fmul2(v1[i], make_float2(f2, f2));
+      for (int k = 0; k < 4; ++k) {
+        v0[k] = fmul2(v0[k], make_float2(f2, f2));
+        v1[k] = fmul2(v1[k], make_float2(f2, f2));
       }
     }
     uint32_t o0[2], o1[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float2 p = v0[2 * i], q = v0[2 * i + 1], y = v1[2 * i], z = v1[2 * i + 1];
+    for (int k = 0; k < 2; ++k) {
+      const float2 p = v0[2 * k], q = v0[2 * k + 1], y = v1[2 * k], z = v1[2 * k + 1];
       if (apart) {
-        o0[i] = pack_e4m3x4(p.x, p.y, q.x, q.y);
-        o1[i] = pack_e4m3x4(y.x, y.y, z.x, z.y);
-      } else {   // elements 8i .. 8i + 7 of the chunk
-        o0[i] = pack_e4m3x4(p.x, y.x, p.y, y.y);
-        o1[i] = pack_e4m3x4(q.x, z.x, q.y, z.y);
+        o0[k] = pack_e4m3x4(p.x, p.y, q.x, q.y);
+        o1[k] = pack_e4m3x4(y.x, y.y, z.x, z.y);
+      } else {   // elements 8k .. 8k + 7 of the chunk
+        o0[k] = pack_e4m3x4(p.x, y.x, p.y, y.y);
+        o1[k] = pack_e4m3x4(q.x, z.x, q.y, z.y);
       }
     }
-    uint8_t* dst = x8 + (r0 + r) * D;
+    uint8_t* dst = out + i * RSTEP * D;
     if (apart) {
       *reinterpret_cast<uint2*>(dst + e0) = make_uint2(o0[0], o0[1]);
       *reinterpret_cast<uint2*>(dst + e1) = make_uint2(o1[0], o1[1]);
@@ -265,7 +301,7 @@ cudaError_t launch_append_dim(const AppendArgs& a, dim3 grid, cudaStream_t st) {
     const cudaError_t e = smem_attr_once<append_kernel<T, D>>(128 * D * 2);
     if (e != cudaSuccess) return e;
   }
-  append_kernel<T, D><<<grid, 256, bytes, st>>>(a);
+  append_kernel<T, D><<<grid, kThreads, bytes, st>>>(a);
   return cudaGetLastError();
 }
 
