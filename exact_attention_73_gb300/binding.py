@@ -108,13 +108,28 @@ def load(build_if_missing: bool = True):
 _DEVICE_TYPE = "cuda"
 
 
-def _ptr(t, name="tensor", numel=None, dtype=None, shape=None):
+def _current_device():
+    """Index of the device the library launches on (what Tensor.get_device gives for a tensor there)."""
+    return torch.cuda.current_device() if _DEVICE_TYPE == "cuda" else -1
+
+
+def _not_here(t, name, dev):
+    if t.device.type != _DEVICE_TYPE:
+        return ValueError(f"{name} must be a {_DEVICE_TYPE} tensor, not on {t.device}")
+    return ValueError(f"{name} is on {t.device}, but cuda:{dev} is the current device")
+
+
+def _ptr(t, name="tensor", numel=None, dtype=None, shape=None, dev=None):
+    """Checked pointer; dev: the device index the tensor has to be on (None: any GPU)."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if not t.is_cuda if _DEVICE_TYPE == "cuda" else t.device.type != _DEVICE_TYPE:
-        raise ValueError(f"{name} must be a {_DEVICE_TYPE} tensor, not on {t.device}")
+    if dev is None:
+        if not t.is_cuda if _DEVICE_TYPE == "cuda" else t.device.type != _DEVICE_TYPE:
+            raise ValueError(f"{name} must be a {_DEVICE_TYPE} tensor, not on {t.device}")
+    elif t.get_device() != dev:
+        raise _not_here(t, name, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (the library reads it as a dense array)")
     if dtype is not None and t.dtype != dtype:
@@ -136,17 +151,18 @@ def _nb(n):
     return (n + 127) // 128
 
 
-def _bwd_ptrs(q, k, v, o, lse, dout, dq, dk, dv):
+def _bwd_ptrs(q, k, v, o, lse, dout, dq, dk, dv, dev=None):
     """Pointers of a dense backward call: q [B,Hq,N,d], k/v [B,Hkv,N,d], o, dout,
     dq like q, dk/dv like k (all of q's type), lse [B,Hq,N] float32."""
     B, Hq, N, d = _dims(q, "q", 4)
     Hkv = _dims(k, "k", 4)[1]
     dt = q.dtype
     kv = (B, Hkv, N, d)
-    return [_ptr(q, "q"), _ptr(k, "k", dtype=dt, shape=kv), _ptr(v, "v", dtype=dt, shape=kv),
-            _ptr(o, "o", q.numel(), dt), _ptr(lse, "lse", B * Hq * N, torch.float32),
-            _ptr(dout, "dout", q.numel(), dt), _ptr(dq, "dq", q.numel(), dt), _ptr(dk, "dk", k.numel(), dt),
-            _ptr(dv, "dv", k.numel(), dt)]
+    nq, nk = q.numel(), k.numel()
+    return [_ptr(q, "q", None, None, None, dev), _ptr(k, "k", None, dt, kv, dev), _ptr(v, "v", None, dt, kv, dev),
+            _ptr(o, "o", nq, dt, None, dev), _ptr(lse, "lse", B * Hq * N, torch.float32, None, dev),
+            _ptr(dout, "dout", nq, dt, None, dev), _ptr(dq, "dq", nq, dt, None, dev), _ptr(dk, "dk", nk, dt, None, dev),
+            _ptr(dv, "dv", nk, dt, None, dev)]
 
 
 # the current stream's handle without building a Stream object (4 us a call, as much as the launch itself)
@@ -175,14 +191,15 @@ def _dtype(t):
     return _DT[t.dtype]
 
 
-def _fwd_ptrs(q, k, v, o, lse):
+def _fwd_ptrs(q, k, v, o, lse, dev=None):
     """Pointers of a dense forward call: q [B,Hq,N,d], k/v [B,Hkv,N,d] of q's
     type, o like q, lse [B,Hq,N] float32."""
     B, Hq, N, d = _dims(q, "q", 4)
     Hkv = _dims(k, "k", 4)[1]
     kv = (B, Hkv, N, d)
-    return [_ptr(q, "q"), _ptr(k, "k", dtype=q.dtype, shape=kv), _ptr(v, "v", dtype=q.dtype, shape=kv),
-            _ptr(o, "o", q.numel(), q.dtype), _ptr(lse, "lse", B * Hq * N, torch.float32)]
+    dt = q.dtype
+    return [_ptr(q, "q", None, None, None, dev), _ptr(k, "k", None, dt, kv, dev), _ptr(v, "v", None, dt, kv, dev),
+            _ptr(o, "o", q.numel(), dt, None, dev), _ptr(lse, "lse", B * Hq * N, torch.float32, None, dev)]
 
 
 def attn_fwd(q, k, v, o, lse, scale=None, causal=False, stream=None):
@@ -330,24 +347,11 @@ def attn_decode_fp8(q8, sq, k8, v8, sk, sv, o, lse, workspace, num_splits, seqle
                                   B, Hq, Hkv, Nmax, d, scale, int(num_splits), _stream(stream)), "attn_decode_fp8")
 
 
-def _one_device(*tensors):
-    """Every tensor on the current device: the stream and the library's launches are there."""
-    if _DEVICE_TYPE != "cuda":
-        return
-    current = None
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and t.is_cuda:
-            if current is None:
-                current = torch.cuda.current_device()
-            if t.get_device() != current:
-                raise ValueError(f"tensor on {t.device}, but cuda:{current} is the current device")
-
-
-def _strided(t, name, dtype=None, shape=None):
+def _strided(t, name, dev, dtype=None, shape=None):
     """Pointer and strides of a [B, H, N, d] tensor whose rows are dense (any batch, head and row strides)."""
     b, h, n, d = _dims(t, name, 4)
-    if not t.is_cuda if _DEVICE_TYPE == "cuda" else t.device.type != _DEVICE_TYPE:
-        raise ValueError(f"{name} must be a {_DEVICE_TYPE} tensor, not on {t.device}")
+    if t.get_device() != dev:
+        raise _not_here(t, name, dev)
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
@@ -359,11 +363,11 @@ def _strided(t, name, dtype=None, shape=None):
     return t.data_ptr(), _Strides(sb if b > 1 else 0, sh if h > 1 else 0, sn if n > 1 else 0)
 
 
-def _rope_dims(rope_cos, rope_sin):
+def _rope_dims(rope_cos, rope_sin, dev):
     """Tables [n_pos, rot_dim / 2]: their pointers, rot_dim and n_pos."""
     n_pos, half = _dims(rope_cos, "rope_cos", 2)
-    return (_ptr(rope_cos, "rope_cos", dtype=torch.float32),
-            _ptr(rope_sin, "rope_sin", dtype=torch.float32, shape=(n_pos, half)), 2 * half, n_pos)
+    return (_ptr(rope_cos, "rope_cos", None, torch.float32, None, dev),
+            _ptr(rope_sin, "rope_sin", None, torch.float32, (n_pos, half), dev), 2 * half, n_pos)
 
 
 def attn_rope(x, y, rope_cos, rope_sin, positions=None, interleaved=False, inverse=False, stream=None):
@@ -372,32 +376,31 @@ def attn_rope(x, y, rope_cos, rope_sin, positions=None, interleaved=False, inver
     Tables float32 [n_pos, rot_dim/2]; positions int32 [B,N] or None (row n at position n; a negative
     one leaves its row of y as it was). inverse turns back: the backward pass of the rotation."""
     B, H, N, d = _dims(x, "x", 4)
-    _one_device(x, y, rope_cos, rope_sin, positions)
-    px, sx = _strided(x, "x")
-    py, sy = _strided(y, "y", x.dtype, x.shape)
-    pc, ps, rot, n_pos = _rope_dims(rope_cos, rope_sin)
-    _check(load().attn_rope(px, py, pc, ps, _ptr(positions, "positions", dtype=torch.int32, shape=(B, N)), sx, sy,
-                            B, H, N, d, rot, n_pos, int(bool(interleaved)), int(bool(inverse)), _dtype(x),
+    dev = _current_device()
+    px, sx = _strided(x, "x", dev)
+    py, sy = _strided(y, "y", dev, x.dtype, x.shape)
+    pc, ps, rot, n_pos = _rope_dims(rope_cos, rope_sin, dev)
+    _check(load().attn_rope(px, py, pc, ps, _ptr(positions, "positions", None, torch.int32, (B, N), dev), sx, sy, B, H, N, d, rot, n_pos, int(bool(interleaved)), int(bool(inverse)), _dtype(x),
                             _stream(stream)), "attn_rope")
 
 
 def attn_rope_tables(rope_cos, rope_sin, inv_freq, first_position=0, amplitude=1.0, stream=None):
     """Cosine and sine tables [n_pos, rot_dim/2] float32 of positions first_position, + 1, ...;
     inv_freq float64 [rot_dim/2] on the device (see rope.inv_freq for the usual scalings)."""
-    _one_device(rope_cos, rope_sin, inv_freq)
-    pc, ps, rot, n_pos = _rope_dims(rope_cos, rope_sin)
-    _check(load().attn_rope_tables(pc, ps, _ptr(inv_freq, "inv_freq", rot // 2, torch.float64), int(first_position),
-                                   n_pos, rot, float(amplitude), _stream(stream)), "attn_rope_tables")
+    dev = _current_device()
+    pc, ps, rot, n_pos = _rope_dims(rope_cos, rope_sin, dev)
+    _check(load().attn_rope_tables(pc, ps, _ptr(inv_freq, "inv_freq", rot // 2, torch.float64, None, dev),
+                                   int(first_position), n_pos, rot, float(amplitude), _stream(stream)), "attn_rope_tables")
 
 
 def attn_mask_rows(row_ranges, doc_ids=None, prefix_lens=None, causal=True, stream=None):
     """Visible keys [lo, hi) of every row into row_ranges int32 [B,N,2]: doc_ids int32 [B,N] (runs of
     equal ids; negative: padding), prefix_lens int32 [B] (keys below are seen by their whole document)."""
     B, N, _ = _dims(row_ranges, "row_ranges", 3)
-    _one_device(row_ranges, doc_ids, prefix_lens)
-    _check(load().attn_mask_rows(_ptr(doc_ids, "doc_ids", dtype=torch.int32, shape=(B, N)),
-                                 _ptr(prefix_lens, "prefix_lens", B, torch.int32),
-                                 _ptr(row_ranges, "row_ranges", dtype=torch.int32, shape=(B, N, 2)), B, N,
+    dev, i32 = _current_device(), torch.int32
+    _check(load().attn_mask_rows(_ptr(doc_ids, "doc_ids", None, i32, (B, N), dev),
+                                 _ptr(prefix_lens, "prefix_lens", B, i32, None, dev),
+                                 _ptr(row_ranges, "row_ranges", None, i32, (B, N, 2), dev), B, N,
                                  int(bool(causal)), _stream(stream)), "attn_mask_rows")
 
 
@@ -411,12 +414,13 @@ def attn_fwd_score(q, k, v, o, lse, workspace=None, row_ranges=None, slopes=None
     int32 [B,N,2] (these need a workspace of attn_score_workspace_size bytes); slopes fp32 [Hq]."""
     B, Hq, N, d = _dims(q, "q", 4)
     Hkv = _dims(k, "k", 4)[1]
-    _one_device(q, k, v, o, lse, workspace, row_ranges, slopes)
+    dev = _current_device()
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     left, right = (int(w) for w in window)
-    _check(load().attn_fwd_score(*_fwd_ptrs(q, k, v, o, lse),
-                                 _ptr(row_ranges, "row_ranges", dtype=torch.int32, shape=(B, N, 2)),
-                                 _ptr(slopes, "slopes", Hq, torch.float32), _ptr(workspace, "workspace"),
+    _check(load().attn_fwd_score(*_fwd_ptrs(q, k, v, o, lse, dev),
+                                 _ptr(row_ranges, "row_ranges", None, torch.int32, (B, N, 2), dev),
+                                 _ptr(slopes, "slopes", Hq, torch.float32, None, dev),
+                                 _ptr(workspace, "workspace", None, None, None, dev),
                                  0 if workspace is None else workspace.numel() * workspace.element_size(), B, Hq, Hkv,
                                  N, d, scale, float(score_cap), left, right, _dtype(q), _stream(stream)),
            "attn_fwd_score")
@@ -431,17 +435,18 @@ def attn_bwd_score(q, k, v, o, lse, dout, dq, dk, dv, workspace, row_ranges=None
     """Backward of attn_fwd_score; workspace of attn_bwd_score_workspace_size bytes."""
     B, Hq, N, d = _dims(q, "q", 4)
     Hkv = _dims(k, "k", 4)[1]
-    _one_device(q, k, v, o, lse, dout, dq, dk, dv, workspace, row_ranges, slopes)
+    dev = _current_device()
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     left, right = (int(w) for w in window)
-    _check(load().attn_bwd_score(*_bwd_ptrs(q, k, v, o, lse, dout, dq, dk, dv),
-                                 _ptr(row_ranges, "row_ranges", dtype=torch.int32, shape=(B, N, 2)),
-                                 _ptr(slopes, "slopes", Hq, torch.float32), _ptr(workspace, "workspace"),
+    _check(load().attn_bwd_score(*_bwd_ptrs(q, k, v, o, lse, dout, dq, dk, dv, dev),
+                                 _ptr(row_ranges, "row_ranges", None, torch.int32, (B, N, 2), dev),
+                                 _ptr(slopes, "slopes", Hq, torch.float32, None, dev),
+                                 _ptr(workspace, "workspace", None, None, None, dev),
                                  workspace.numel() * workspace.element_size(), B, Hq, Hkv, N, d, scale,
                                  float(score_cap), left, right, _dtype(q), _stream(stream)), "attn_bwd_score")
 
 
-def _cache_ptrs(k8, v8, sk, sv, block_table, B, Hkv, d):
+def _cache_ptrs(k8, v8, sk, sv, block_table, B, Hkv, d, dev):
     """Checked pointers of a cache (k8, v8, sk, sv, block_table), its rows per sequence and its pages:
     dense k8 [B,Hkv,Nmax,d], or pages [P,Hkv,128,d] with block_table [B,blocks]."""
     shape = _dims(k8, "k8", 4)
@@ -455,9 +460,9 @@ def _cache_ptrs(k8, v8, sk, sv, block_table, B, Hkv, d):
         rows, pages, want = 128 * blocks, shape[0], (shape[0], Hkv, 128, d)
         factors = (pages, Hkv)
     u8, f32 = torch.uint8, torch.float32
-    return (_ptr(k8, "k8", dtype=u8, shape=want), _ptr(v8, "v8", dtype=u8, shape=want),
-            _ptr(sk, "sk", dtype=f32, shape=factors), _ptr(sv, "sv", dtype=f32, shape=factors),
-            _ptr(block_table, "block_table", dtype=torch.int32)), rows, pages
+    return (_ptr(k8, "k8", None, u8, want, dev), _ptr(v8, "v8", None, u8, want, dev),
+            _ptr(sk, "sk", None, f32, factors, dev), _ptr(sv, "sv", None, f32, factors, dev),
+            _ptr(block_table, "block_table", None, torch.int32, None, dev)), rows, pages
 
 
 def attn_cache_append_fp8(k, v, k8, v8, sk, sv, seqlens, new_lens=None, block_table=None, rope_cos=None,
@@ -467,16 +472,16 @@ def attn_cache_append_fp8(k, v, k8, v8, sk, sv, seqlens, new_lens=None, block_ta
     [P,Hkv,128,d], [P,Hkv] with block_table int32 [B,blocks]. new_lens int32 [B]: rows of k and v that count
     (None: all). Tables given: the keys are rotated first, row r of a sequence at position r."""
     B, Hkv, n, d = _dims(k, "k", 4)
-    _one_device(k, v, k8, v8, sk, sv, seqlens, new_lens, block_table, rope_cos, rope_sin)
-    pk, stk = _strided(k, "k")
-    pv, stv = _strided(v, "v", k.dtype, k.shape)
-    (p8k, p8v, psk, psv, pt), rows, pages = _cache_ptrs(k8, v8, sk, sv, block_table, B, Hkv, d)
+    dev, i32 = _current_device(), torch.int32
+    pk, stk = _strided(k, "k", dev)
+    pv, stv = _strided(v, "v", dev, k.dtype, k.shape)
+    (p8k, p8v, psk, psv, pt), rows, pages = _cache_ptrs(k8, v8, sk, sv, block_table, B, Hkv, d, dev)
     if (rope_cos is None) != (rope_sin is None):
         raise ValueError("rope_cos and rope_sin go together")
-    pc, ps, rot, n_pos = _rope_dims(rope_cos, rope_sin) if rope_cos is not None else (None, None, 0, 0)
+    pc, ps, rot, n_pos = _rope_dims(rope_cos, rope_sin, dev) if rope_cos is not None else (None, None, 0, 0)
     _check(load().attn_cache_append_fp8(pk, pv, stk, stv, p8k, p8v, psk, psv,
-                                        _ptr(seqlens, "seqlens", B, torch.int32),
-                                        _ptr(new_lens, "new_lens", B, torch.int32), pt, pc, ps, B, Hkv, n, rows,
+                                        _ptr(seqlens, "seqlens", B, i32, None, dev),
+                                        _ptr(new_lens, "new_lens", B, i32, None, dev), pt, pc, ps, B, Hkv, n, rows,
                                         pages, d, rot, n_pos, int(bool(interleaved)), _dtype(k), _stream(stream)),
            "attn_cache_append_fp8")
 
@@ -497,14 +502,15 @@ def attn_decode_cache_fp8(q, k8, v8, sk, sv, seqlens, o, lse, workspace, num_spl
     slopes fp32 [Hq], score_cap and window_left as attn_fwd_score."""
     B, Hq, d = _dims(q, "q", 3)
     Hkv = _dims(k8, "k8", 4)[1]
-    _one_device(q, k8, v8, sk, sv, seqlens, o, lse, workspace, block_table, slopes)
-    (p8k, p8v, psk, psv, pt), rows, pages = _cache_ptrs(k8, v8, sk, sv, block_table, B, Hkv, d)
+    dev, f32 = _current_device(), torch.float32
+    (p8k, p8v, psk, psv, pt), rows, pages = _cache_ptrs(k8, v8, sk, sv, block_table, B, Hkv, d, dev)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
-    _check(load().attn_decode_cache_fp8(_ptr(q, "q"), p8k, p8v, psk, psv, pt,
-                                        _ptr(seqlens, "seqlens", B, torch.int32),
-                                        _ptr(slopes, "slopes", Hq, torch.float32),
-                                        _ptr(o, "o", dtype=q.dtype, shape=(B, Hq, d)),
-                                        _ptr(lse, "lse", B * Hq, torch.float32), _ptr(workspace, "workspace"),
+    _check(load().attn_decode_cache_fp8(_ptr(q, "q", None, None, None, dev), p8k, p8v, psk, psv, pt,
+                                        _ptr(seqlens, "seqlens", B, torch.int32, None, dev),
+                                        _ptr(slopes, "slopes", Hq, f32, None, dev),
+                                        _ptr(o, "o", None, q.dtype, (B, Hq, d), dev),
+                                        _ptr(lse, "lse", B * Hq, f32, None, dev),
+                                        _ptr(workspace, "workspace", None, None, None, dev),
                                         workspace.numel() * workspace.element_size(), B, Hq, Hkv, rows, pages, d,
                                         scale, float(score_cap), int(window_left), int(num_splits), _dtype(q),
                                         _stream(stream)), "attn_decode_cache_fp8")

@@ -129,11 +129,8 @@ __global__ void __launch_bounds__(256) mask_rows_kernel(const int* __restrict__ 
   }
 }
 
-// One warp per 64 rows.
-__global__ void __launch_bounds__(256) score_bounds_kernel(const int2* __restrict__ ranges, int2* __restrict__ bounds,
-                                                           int N, int ntile, int left, int right) {
-  const int i = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, b = blockIdx.y;
-  if (i >= ntile) return;
+// Union of the visible keys of 64-row tile i of sequence b, by one warp.
+__device__ __forceinline__ int2 tile_bounds(const int2* ranges, int b, int i, int N, int left, int right, int lane) {
   int2 v = make_int2(N, 0);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
@@ -145,17 +142,13 @@ __global__ void __launch_bounds__(256) score_bounds_kernel(const int2* __restric
   }
   v.x = __reduce_min_sync(0xffffffffu, v.x);
   v.y = __reduce_max_sync(0xffffffffu, v.y);
-  if (lane == 0) bounds[static_cast<long long>(b) * ntile + i] = v;
+  return v;
 }
-
-// One warp per 128 keys: the first and last 64-row tile with a row that may see one.
-__global__ void __launch_bounds__(256) score_key_tiles_kernel(const int2* __restrict__ bounds, int2* __restrict__ key_tiles,
-                                                              int ntile, int nkey) {
-  const int j = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, b = blockIdx.y;
-  if (j >= nkey) return;
+// The 64-row tiles of a sequence (bounds) with a row that may see one of keys 128j .., by one warp.
+__device__ __forceinline__ int2 tiles_of_keys(const int2* bounds, int j, int ntile, int lane) {
   int lo = ntile, hi = 0;
   for (int i = lane; i < ntile; i += 32) {
-    const int2 v = bounds[static_cast<long long>(b) * ntile + i];
+    const int2 v = bounds[i];
     if (v.x < (j + 1) * 128 && v.y > j * 128) {
       lo = min(lo, i);
       hi = max(hi, i + 1);
@@ -167,20 +160,41 @@ __global__ void __launch_bounds__(256) score_key_tiles_kernel(const int2* __rest
     lo = 0;
     hi = 1;
   }
-  if (lane == 0) key_tiles[static_cast<long long>(b) * nkey + j] = make_int2(lo, hi);
+  return make_int2(lo, hi);
+}
+
+// One warp per 64 rows.
+__global__ void __launch_bounds__(256) score_bounds_kernel(const int2* __restrict__ ranges, int2* __restrict__ bounds,
+                                                           int N, int ntile, int left, int right) {
+  const int i = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, b = blockIdx.y;
+  if (i >= ntile) return;
+  const int2 v = tile_bounds(ranges, b, i, N, left, right, lane);
+  if (lane == 0) bounds[static_cast<long long>(b) * ntile + i] = v;
+}
+
+// One warp per 128 keys.
+__global__ void __launch_bounds__(256) score_key_tiles_kernel(const int2* __restrict__ bounds, int2* __restrict__ key_tiles,
+                                                              int ntile, int nkey) {
+  const int j = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, b = blockIdx.y;
+  if (j >= nkey) return;
+  const int2 v = tiles_of_keys(bounds + static_cast<long long>(b) * ntile, j, ntile, lane);
+  if (lane == 0) key_tiles[static_cast<long long>(b) * nkey + j] = v;
 }
 
 // Counting sort of the units (x, b), x < nx, by their tiles, most first, in
-// kBins levels of work (`most` tiles: the highest). group > 0: unit x unites
-// `group` 64-row tiles of `facts` (the forward's bounds, work in KV tiles);
-// group = 0: facts[b * nx + x] is the unit's walk (the backward's key tiles).
+// kBins levels of work (`most` tiles: the highest), by one CTA. group > 0:
+// unit x unites `group` 64-row tiles of `facts` (the forward's bounds, work in
+// KV tiles); group = 0: facts[b * nx + x] is the unit's walk (the backward's
+// key tiles).
 constexpr int kBins = 1024;
-__global__ void __launch_bounds__(kBins) score_order_kernel(const int2* __restrict__ facts, int2* __restrict__ order,
-                                                            int B, int nx, int group, int ntile, int most) {
-  __shared__ int count[kBins];
-  __shared__ int warp_sum[32];
+struct OrderSmem {
+  int count[kBins];
+  int warp_sum[32];
+};
+__device__ __forceinline__ void sort_units(OrderSmem& sm, const int2* facts, int2* order, int B, int nx, int group,
+                                           int ntile, int most) {
   const int t = threadIdx.x, lane = t & 31;
-  count[t] = 0;
+  sm.count[t] = 0;
   __syncthreads();
   const long long units = static_cast<long long>(B) * nx;
   auto level = [&](long long u) {
@@ -200,23 +214,50 @@ __global__ void __launch_bounds__(kBins) score_order_kernel(const int2* __restri
     }
     return kBins - 1 - static_cast<int>(static_cast<long long>(min(work, most)) * (kBins - 1) / most);
   };
-  for (long long u = t; u < units; u += kBins) atomicAdd(&count[level(u)], 1);
+  for (long long u = t; u < units; u += kBins) atomicAdd(&sm.count[level(u)], 1);
   __syncthreads();
   // exclusive prefix sum over the levels
-  const int n = count[t];
+  const int n = sm.count[t];
   int s = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += y;
   }
-  if (lane == 31) warp_sum[t >> 5] = s;
+  if (lane == 31) sm.warp_sum[t >> 5] = s;
   __syncthreads();
-  for (int w = 0; w < (t >> 5); ++w) s += warp_sum[w];
-  count[t] = s - n;
+  for (int w = 0; w < (t >> 5); ++w) s += sm.warp_sum[w];
+  sm.count[t] = s - n;
   __syncthreads();
   for (long long u = t; u < units; u += kBins)
-    order[atomicAdd(&count[level(u)], 1)] = make_int2(static_cast<int>(u % nx), static_cast<int>(u / nx));
+    order[atomicAdd(&sm.count[level(u)], 1)] = make_int2(static_cast<int>(u % nx), static_cast<int>(u / nx));
+}
+__global__ void __launch_bounds__(kBins) score_order_kernel(const int2* facts, int2* order, int B, int nx, int group,
+                                                            int ntile, int most) {
+  __shared__ OrderSmem sm;
+  sort_units(sm, facts, order, B, nx, group, ntile, most);
+}
+
+// Few rows: bounds, key tiles (nkey > 0) and order by one CTA, in place of
+// two or three launches.
+constexpr int kFactsRows = 16384;
+__global__ void __launch_bounds__(kBins) score_facts_kernel(const int2* __restrict__ ranges, int2* bounds,
+                                                            int2* key_tiles, int2* order, int B, int N, int ntile,
+                                                            int nkey, int nx, int group, int left, int right) {
+  __shared__ OrderSmem sm;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int u = warp; u < B * ntile; u += 32) {
+    const int2 v = tile_bounds(ranges, u / ntile, u % ntile, N, left, right, lane);
+    if (lane == 0) bounds[u] = v;
+  }
+  __syncthreads();
+  for (int u = warp; u < B * nkey; u += 32) {
+    const int2 v = tiles_of_keys(bounds + (u / nkey) * ntile, u % nkey, ntile, lane);
+    if (lane == 0) key_tiles[u] = v;
+  }
+  __syncthreads();
+  if (nkey > 0) sort_units(sm, key_tiles, order, B, nkey, 0, ntile, ntile);
+  else sort_units(sm, bounds, order, B, nx, group, ntile, (N + 127) / 128);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -248,6 +289,11 @@ cudaError_t prepare_score(ScoreArgs& a, const int* row_ranges, const float* slop
   a.bounds = bounds;
   a.key_tiles = kt;
   a.order = order;
+  if (static_cast<long long>(B) * N <= kFactsRows) {
+    score_facts_kernel<<<1, kBins, 0, st>>>(a.ranges, bounds, kt, order, B, N, a.ntile, keys ? nkeys(N) : 0,
+                                            keys ? 0 : (N + unit_rows - 1) / unit_rows, unit_rows / 64, left, right);
+    return cudaGetLastError();
+  }
   score_bounds_kernel<<<dim3((a.ntile + 7) / 8, B), 256, 0, st>>>(a.ranges, bounds, N, a.ntile, left, right);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
