@@ -29,6 +29,9 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const T* __restrict__ o, c
   constexpr int c = D / 32;
   const long long r = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  // as a programmatic dependent this grid must not end before the one it runs
+  // beside (whoever waits for this one waits for both): its last CTA sees to it
+  if (blockIdx.x == gridDim.x - 1) grid_wait_prerequisites();
   if (r >= rows) return;
   const T* po = o + r * D + lane * c;
   const T* pd = dout + r * D + lane * c;
@@ -162,26 +165,33 @@ cudaError_t launch_main_dt(int dt, int hd, const CUtensorMap& k, const CUtensorM
 
 }  // namespace
 
+// `beside`: the row sums run as a programmatic dependent beside the launch
+// before them, whose results they do not read; their grid ends after it.
+template <typename T, int D>
+static cudaError_t launch_pre(const void* o, const void* dout, float* dvec, float* dq_acc, long long rows, int Hq,
+                              int T_tokens, int packed, cudaStream_t st, bool beside) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, bwd_pre_kernel<T, D>, static_cast<const T*>(o), static_cast<const T*>(dout), dvec,
+                            dq_acc, rows, Hq, T_tokens, packed);
+}
+
 cudaError_t launch_bwd_pre(int dt, int d, const void* o, const void* dout, float* dvec, float* dq_acc, long long rows,
-                           int Hq, int T_tokens, int packed, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>((rows + 7) / 8));
-  const auto* ob = static_cast<const __nv_bfloat16*>(o);
-  const auto* db = static_cast<const __nv_bfloat16*>(dout);
-  const auto* oh = static_cast<const __half*>(o);
-  const auto* dh = static_cast<const __half*>(dout);
-  if (d == 128) {
-    if (dt == kBF16) bwd_pre_kernel<__nv_bfloat16, 128><<<grid, 256, 0, st>>>(ob, db, dvec, dq_acc, rows, Hq, T_tokens, packed);
-    else bwd_pre_kernel<__half, 128><<<grid, 256, 0, st>>>(oh, dh, dvec, dq_acc, rows, Hq, T_tokens, packed);
-  } else if (d == 64) {
-    if (dt == kBF16) bwd_pre_kernel<__nv_bfloat16, 64><<<grid, 256, 0, st>>>(ob, db, dvec, dq_acc, rows, Hq, T_tokens, packed);
-    else bwd_pre_kernel<__half, 64><<<grid, 256, 0, st>>>(oh, dh, dvec, dq_acc, rows, Hq, T_tokens, packed);
-  } else if (d == 256) {
-    if (dt == kBF16) bwd_pre_kernel<__nv_bfloat16, 256><<<grid, 256, 0, st>>>(ob, db, dvec, dq_acc, rows, Hq, T_tokens, packed);
-    else bwd_pre_kernel<__half, 256><<<grid, 256, 0, st>>>(oh, dh, dvec, dq_acc, rows, Hq, T_tokens, packed);
-  } else {
-    return cudaErrorInvalidValue;
+                           int Hq, int T_tokens, int packed, cudaStream_t st, bool beside) {
+  const bool bf = dt == kBF16;
+  switch (d) {
+    case 64: return (bf ? launch_pre<__nv_bfloat16, 64> : launch_pre<__half, 64>)(o, dout, dvec, dq_acc, rows, Hq, T_tokens, packed, st, beside);
+    case 128: return (bf ? launch_pre<__nv_bfloat16, 128> : launch_pre<__half, 128>)(o, dout, dvec, dq_acc, rows, Hq, T_tokens, packed, st, beside);
+    case 256: return (bf ? launch_pre<__nv_bfloat16, 256> : launch_pre<__half, 256>)(o, dout, dvec, dq_acc, rows, Hq, T_tokens, packed, st, beside);
+    default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 cudaError_t launch_bwd_main(int dt, int d, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,

@@ -186,7 +186,7 @@ __device__ __forceinline__ bool fwd_unit(const FwdArgs& a, int lin, FwdUnit& w) 
   if constexpr ((kScore & kScoreRanges) != 0) {
     int pos;
     heavy_first_map(8, lin, a.ux * a.uz, a.uy, 1, pos, by, bz);
-    const int2 u = __ldg(a.sc.order + pos);
+    const int2 u = a.sc.order[pos];   // not through the read-only path: written while this grid sets itself up
     bx = u.x;
     bz = u.y;
   } else if (a.causal) {
@@ -221,7 +221,7 @@ __device__ __forceinline__ bool fwd_unit(const FwdArgs& a, int lin, FwdUnit& w) 
     klo = w.L;
     khi = 0;
     for (int i = w.qt0 * 2; i < min((w.qt0 + QT) * 2, a.sc.ntile); ++i) {
-      const int2 t = __ldg(a.sc.bounds + static_cast<long long>(w.b) * a.sc.ntile + i);
+      const int2 t = a.sc.bounds[static_cast<long long>(w.b) * a.sc.ntile + i];
       klo = min(klo, t.x);
       khi = max(khi, t.y);
     }
@@ -269,7 +269,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const bool packed = a.cu_seqlens != nullptr;
-  {   // a CTA whose units hold no query row leaves before any set-up
+  if constexpr ((kScore & kScoreRanges) == 0) {   // a CTA whose units hold no query row leaves before any set-up
     bool any = false;
     FwdUnit w;
     for (int k = 0; !any; ++k) {
@@ -306,6 +306,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
+  if constexpr ((kScore & kScoreRanges) != 0) grid_wait_prerequisites();   // the tile facts
 
   // Every role walks the same units in the same order. Barrier phases run on
   // across units: q_full, q_empty and o_final once per unit, s_full and

@@ -27,7 +27,7 @@ struct BwdArgs;
 bool operand_map(CUtensorMap* m, const void* base, int dt, int d, bool packed, int B, int H, long long rows,
                  int box_rows);
 cudaError_t launch_bwd_pre(int dt, int d, const void* o, const void* dout, float* dvec, float* dq_acc,
-                           long long rows, int Hq, int T_tokens, int packed, cudaStream_t st);
+                           long long rows, int Hq, int T_tokens, int packed, cudaStream_t st, bool beside = false);
 cudaError_t launch_bwd_main(int dt, int d, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
                             const CUtensorMap& dout, const CUtensorMap& dq_acc, const BwdArgs& a, int max_len, int nz,
                             cudaStream_t st);

@@ -12,7 +12,9 @@
 // KV range. Per 128 keys the 64-row tiles that see one of them: the
 // backward's walk. From these the order of the units, most work first (a
 // counting sort): with documents the work of neighbouring tiles differs by
-// their length, and a long one started last would run alone.
+// their length, and a long one started last would run alone. The kernel behind
+// them is a programmatic dependent: the forward sets itself up meanwhile, and
+// the backward's row sums, which need no facts, run beside them.
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -36,53 +38,58 @@ __global__ void __launch_bounds__(256) mask_rows_kernel(const int* __restrict__ 
   const int c0 = blockIdx.x * kMaskRows, c1 = min(c0 + kMaskRows, N);
   const int r0 = c0 + 4 * t;
   int start[4], end[4], id[4];
+  int edge_lo = 0, edge_hi = N;
   if (ids) {
     ids += static_cast<long long>(b) * N;
-    // start of the run that reaches back over c0 - 1, end of the one that goes on past c1
-    if (t < 2) edge[t] = t == 0 ? c0 : c1;
-    __syncthreads();
     const int first = ids[c0], last = ids[c1 - 1];
-    for (int hi = c0; hi > 0; hi -= 256) {   // rows hi - 256 .. hi - 1
-      const int r = hi - 1 - t;
-      const int differs = r >= 0 && ids[r] != first;
-      const int any = __syncthreads_or(differs);
-      if (any) {
-        if (t == 0) edge[0] = 0;
-        __syncthreads();
-        if (differs) atomicMax(&edge[0], r + 1);
-        break;
-      }
-      if (t == 0) edge[0] = max(hi - 256, 0);
-    }
+    const int before_id = r0 > c0 && r0 < c1 ? ids[r0 - 1] : 0, behind_id = r0 + 4 < c1 ? ids[r0 + 4] : 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) id[u] = r0 + u < c1 ? ids[r0 + u] : 0;
+    // start of the run that reaches back over c0 - 1, end of the one that goes
+    // on past c1: both searches together, 1024 ids a step on either side
+    int hi = c0, lo = c1;
+    bool back = hi > 0, ahead = lo < N;
+    edge_lo = c0;
+    edge_hi = c1;
+    if (t < 2) edge[t] = t == 0 ? -1 : INT_MAX;
     __syncthreads();
-    for (int lo = c1; lo < N; lo += 256) {
-      const int r = lo + t;
-      const int differs = r < N && ids[r] != last;
-      const int any = __syncthreads_or(differs);
-      if (any) {
-        if (t == 0) edge[1] = N;
-        __syncthreads();
-        if (differs) atomicMin(&edge[1], r);
-        break;
+    while (back || ahead) {
+      int s = -1, e = INT_MAX;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int rb = hi - 1 - t - 256 * q, ra = lo + t + 256 * q;
+        if (back && rb >= 0 && ids[rb] != first) s = max(s, rb + 1);
+        if (ahead && ra < N && ids[ra] != last) e = min(e, ra);
       }
-      if (t == 0) edge[1] = min(lo + 256, N);
+      s = __reduce_max_sync(0xffffffffu, s);
+      e = __reduce_min_sync(0xffffffffu, e);
+      if (lane == 0 && s >= 0) atomicMax(&edge[0], s);
+      if (lane == 0 && e < INT_MAX) atomicMin(&edge[1], e);
+      hi -= kMaskRows;
+      lo += kMaskRows;
+      __syncthreads();
+      if (back && (edge[0] >= 0 || hi <= 0)) {
+        edge_lo = max(edge[0], 0);
+        back = false;
+      }
+      if (ahead && (edge[1] < INT_MAX || lo >= N)) {
+        edge_hi = min(edge[1], N);
+        ahead = false;
+      }
+      __syncthreads();   // read by all before the next step
     }
-    __syncthreads();
-    const int edge_lo = edge[0], edge_hi = edge[1];
     // changes inside the CTA's rows: row r starts a run if its id differs from row r - 1's
     int s = -1, e = INT_MAX;                  // last start of this thread's rows, first end
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int r = r0 + u;
-      id[u] = r < c1 ? ids[r] : 0;
-      const bool starts = r < c1 && r > c0 && ids[r - 1] != id[u];
-      if (starts) s = r;
+      if (r < c1 && r > c0 && (u == 0 ? before_id : id[u - 1]) != id[u]) s = r;
       start[u] = s;
     }
 #pragma unroll
     for (int u = 3; u >= 0; --u) {
       const int r = r0 + u;
-      if (r < c1 - 1 && ids[r + 1] != id[u]) e = r + 1;
+      if (r < c1 - 1 && (u == 3 ? behind_id : id[u + 1]) != id[u]) e = r + 1;
       end[u] = e;
     }
     // scans over the threads: the last start before, the first end behind
@@ -93,7 +100,6 @@ __global__ void __launch_bounds__(256) mask_rows_kernel(const int* __restrict__ 
       if (lane >= o) ps = max(ps, a);
       if (lane < 32 - o) pe = min(pe, z);
     }
-    __syncthreads();
     if (lane == 31) red[0][warp] = ps;
     if (lane == 0) red[1][warp] = pe;
     __syncthreads();
@@ -129,8 +135,9 @@ __global__ void __launch_bounds__(256) mask_rows_kernel(const int* __restrict__ 
   }
 }
 
-// Union of the visible keys of 64-row tile i of sequence b, by one warp.
-__device__ __forceinline__ int2 tile_bounds(const int2* ranges, int b, int i, int N, int left, int right, int lane) {
+// Union of the visible keys of a 64-row tile, by one warp: a lane's two rows
+// (tile i of sequence b), then over the lanes.
+__device__ __forceinline__ int2 tile_rows(const int2* ranges, int b, int i, int N, int left, int right, int lane) {
   int2 v = make_int2(N, 0);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
@@ -140,9 +147,10 @@ __device__ __forceinline__ int2 tile_bounds(const int2* ranges, int b, int i, in
     v.x = min(v.x, s.x);
     v.y = max(v.y, s.y);
   }
-  v.x = __reduce_min_sync(0xffffffffu, v.x);
-  v.y = __reduce_max_sync(0xffffffffu, v.y);
   return v;
+}
+__device__ __forceinline__ int2 tile_union(int2 v) {
+  return make_int2(__reduce_min_sync(0xffffffffu, v.x), __reduce_max_sync(0xffffffffu, v.y));
 }
 // The 64-row tiles of a sequence (bounds) with a row that may see one of keys 128j .., by one warp.
 __device__ __forceinline__ int2 tiles_of_keys(const int2* bounds, int j, int ntile, int lane) {
@@ -168,7 +176,7 @@ __global__ void __launch_bounds__(256) score_bounds_kernel(const int2* __restric
                                                            int N, int ntile, int left, int right) {
   const int i = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, b = blockIdx.y;
   if (i >= ntile) return;
-  const int2 v = tile_bounds(ranges, b, i, N, left, right, lane);
+  const int2 v = tile_union(tile_rows(ranges, b, i, N, left, right, lane));
   if (lane == 0) bounds[static_cast<long long>(b) * ntile + i] = v;
 }
 
@@ -191,13 +199,14 @@ struct OrderSmem {
   int count[kBins];
   int warp_sum[32];
 };
+template <typename U>   // holds B * nx + kBins
 __device__ __forceinline__ void sort_units(OrderSmem& sm, const int2* facts, int2* order, int B, int nx, int group,
                                            int ntile, int most) {
   const int t = threadIdx.x, lane = t & 31;
   sm.count[t] = 0;
   __syncthreads();
-  const long long units = static_cast<long long>(B) * nx;
-  auto level = [&](long long u) {
+  const U units = static_cast<U>(B) * nx;
+  auto level = [&](U u) {
     const int b = static_cast<int>(u / nx), x = static_cast<int>(u % nx);
     int work;
     if (group == 0) {
@@ -212,9 +221,11 @@ __device__ __forceinline__ void sort_units(OrderSmem& sm, const int2* facts, int
       }
       work = lo < hi ? ((hi + 127) >> 7) - (lo >> 7) : 1;
     }
-    return kBins - 1 - static_cast<int>(static_cast<long long>(min(work, most)) * (kBins - 1) / most);
+    // at most 2^18 tiles, so the product keeps to 32 bits
+    return kBins - 1 - static_cast<int>(static_cast<uint32_t>(min(work, most) * (kBins - 1)) / static_cast<uint32_t>(most));
   };
-  for (long long u = t; u < units; u += kBins) atomicAdd(&sm.count[level(u)], 1);
+  int lv = 0;   // of this thread's last unit: its only one where there are few
+  for (U u = t; u < units; u += kBins) atomicAdd(&sm.count[lv = level(u)], 1);
   __syncthreads();
   // exclusive prefix sum over the levels
   const int n = sm.count[t];
@@ -229,13 +240,16 @@ __device__ __forceinline__ void sort_units(OrderSmem& sm, const int2* facts, int
   for (int w = 0; w < (t >> 5); ++w) s += sm.warp_sum[w];
   sm.count[t] = s - n;
   __syncthreads();
-  for (long long u = t; u < units; u += kBins)
-    order[atomicAdd(&sm.count[level(u)], 1)] = make_int2(static_cast<int>(u % nx), static_cast<int>(u / nx));
+  for (U u = t; u < units; u += kBins) {
+    if (units > kBins) lv = level(u);
+    order[atomicAdd(&sm.count[lv], 1)] = make_int2(static_cast<int>(u % nx), static_cast<int>(u / nx));
+  }
 }
 __global__ void __launch_bounds__(kBins) score_order_kernel(const int2* facts, int2* order, int B, int nx, int group,
                                                             int ntile, int most) {
   __shared__ OrderSmem sm;
-  sort_units(sm, facts, order, B, nx, group, ntile, most);
+  grid_launch_dependents();
+  sort_units<long long>(sm, facts, order, B, nx, group, ntile, most);
 }
 
 // Few rows: bounds, key tiles (nkey > 0) and order by one CTA, in place of
@@ -245,10 +259,21 @@ __global__ void __launch_bounds__(kBins) score_facts_kernel(const int2* __restri
                                                             int2* key_tiles, int2* order, int B, int N, int ntile,
                                                             int nkey, int nx, int group, int left, int right) {
   __shared__ OrderSmem sm;
+  grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int u = warp; u < B * ntile; u += 32) {
-    const int2 v = tile_bounds(ranges, u / ntile, u % ntile, N, left, right, lane);
-    if (lane == 0) bounds[u] = v;
+  constexpr int U = 4;   // tiles of a warp whose loads are in flight together
+  for (int u0 = warp; u0 < B * ntile; u0 += 32 * U) {
+    int2 v[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int u = u0 + 32 * k;
+      v[k] = u < B * ntile ? tile_rows(ranges, u / ntile, u % ntile, N, left, right, lane) : make_int2(N, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      v[k] = tile_union(v[k]);
+      if (lane == 0 && u0 + 32 * k < B * ntile) bounds[u0 + 32 * k] = v[k];
+    }
   }
   __syncthreads();
   for (int u = warp; u < B * nkey; u += 32) {
@@ -256,8 +281,8 @@ __global__ void __launch_bounds__(kBins) score_facts_kernel(const int2* __restri
     if (lane == 0) key_tiles[u] = v;
   }
   __syncthreads();
-  if (nkey > 0) sort_units(sm, key_tiles, order, B, nkey, 0, ntile, ntile);
-  else sort_units(sm, bounds, order, B, nx, group, ntile, (N + 127) / 128);
+  if (nkey > 0) sort_units<uint32_t>(sm, key_tiles, order, B, nkey, 0, ntile, ntile);
+  else sort_units<uint32_t>(sm, bounds, order, B, nx, group, ntile, (N + 127) / 128);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -444,7 +469,8 @@ extern "C" attn_status attn_bwd_score(const void* q, const void* k, const void* 
   a.status = status;
   cudaError_t e = prepare_score(a.sc, row_ranges, slopes, scale, score_cap, B, N, window_left, window_right, facts, 0, true,
                                 st);
-  if (e == cudaSuccess) e = launch_bwd_pre(dtype, d, o, dout, dvec, dq_acc, static_cast<long long>(rows), Hq, N, 0, st);
+  if (e == cudaSuccess) e = launch_bwd_pre(dtype, d, o, dout, dvec, dq_acc, static_cast<long long>(rows), Hq, N, 0, st,
+                                              row_ranges != nullptr);
   if (e == cudaSuccess)
     e = d == 64    ? launch_bwd_score_64(mode, dtype, tk, tv, tq, tdo, tdq, a, N, B, st)
         : d == 128 ? launch_bwd_score_128(mode, dtype, tk, tv, tq, tdo, tdq, a, N, B, st)
