@@ -417,17 +417,33 @@ __device__ __forceinline__ void decode_piece(const CacheDecArgs& a, float* smem,
           }
         }
     }
+    bool add = true;
     if (sv != s_cur) {   // a block with another V factor: O to its units
+      int e = 0;
       if (s_cur != 0.f) {
-        const int e = max(-252, min(252, pow2_exponent(s_cur) - pow2_exponent(sv)));
+        e = max(-252, min(252, pow2_exponent(s_cur) - pow2_exponent(sv)));
+        // O is below 2^50 units (2^25 keys of 2^15 times 448). Where those of a
+        // far smaller factor would overflow, its values are 2^-70 of O: left out.
+        if (e > 60) {
+          float top = 0.f;
 #pragma unroll
-        for (int n = 0; n < NR; ++n)
+          for (int n = 0; n < NR; ++n)
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) acc[n][i][u] = scale_pow2(acc[n][i][u], e);
+              for (int u = 0; u < 4; ++u) top = fmaxf(top, fabsf(acc[n][i][u]));
+          add = !warp_any(scale_pow2(top, e) > 1.2676506002282294e30f);   // 2^100
+        }
+        if (add) {
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) acc[n][i][u] = scale_pow2(acc[n][i][u], e);
+        }
       }
-      s_cur = sv;
+      if (add) s_cur = sv;
     }
     uint32_t pb[NR][KT][2];
 #pragma unroll
@@ -440,8 +456,8 @@ __device__ __forceinline__ void decode_piece(const CacheDecArgs& a, float* smem,
         const float p0 = ex2(x[0] - mu0), p1 = ex2(x[1] - mu1), p2 = ex2(x[2] - mu0), p3 = ex2(x[3] - mu1);
         l[n][0] += p0 + p2;
         l[n][1] += p1 + p3;
-        pb[n][kt][0] = transpose_8x8(pack_f16x2(p0, p1));
-        pb[n][kt][1] = transpose_8x8(pack_f16x2(p2, p3));
+        pb[n][kt][0] = transpose_8x8(add ? pack_f16x2(p0, p1) : 0u);
+        pb[n][kt][1] = transpose_8x8(add ? pack_f16x2(p2, p3) : 0u);
       }
     }
 #pragma unroll

@@ -230,6 +230,28 @@ def test_decode_blocks_with_far_apart_factors():
         assert (np.abs(o.double().cpu().numpy() - ro) <= 2.0 ** -8 * np.abs(ro) + 2.0 ** -10 * mag).all()
 
 
+@pytest.mark.parametrize("tiny", [(1, 2), (0, 1), (2, 4), (4,)])
+def test_decode_factors_past_the_range_of_a_float(tiny):
+    """Values of 1e-37 between values of 1e4: the sum in units of the small ones would pass 2^127."""
+    H, d, n = 2, 128, 640
+    r = np.random.default_rng(34)
+    kv = r.standard_normal((2, 1, H, n, d)).astype(np.float32) * 0.01
+    kv[1] *= 1e6
+    for t in tiny:
+        kv[1, :, :, 128 * t:128 * (t + 1)] *= 1e-41
+    (k8, sk), (v8, sv) = F.quantize_blocks(kv[0]), F.quantize_blocks(kv[1])
+    kf, vf = (F.e4m3_decode(c) * np.repeat(s.astype(np.float64), 128, 2)[..., None] for c, s in ((k8, sk), (v8, sv)))
+    (q,) = inputs.normal(35, [(1, 8, d)])
+    dev = [torch.from_numpy(x).cuda() for x in (k8, v8, sk, sv)]
+    for m in (256, 384, 640):
+        o, lse = torch.empty((1, 8, d), dtype=torch.bfloat16, device="cuda"), torch.empty((1, 8), device="cuda")
+        ws = torch.empty(256, dtype=U8, device="cuda")
+        L.attn_decode_cache_fp8(q.cuda(), *dev, torch.tensor([m], dtype=I32, device="cuda"), o, lse, ws, 1)
+        ro, rl, mag = S.decode(q, kf, vf, [m], d ** -0.5)
+        assert (np.abs(o.double().cpu().numpy() - ro) <= 2.0 ** -8 * np.abs(ro) + 2.0 ** -10 * mag).all()
+        assert np.abs(lse.double().cpu().numpy() - rl).max() <= 1e-5
+
+
 def test_decode_lengths_out_of_range_and_missing_pages():
     B, H, d, nmax = 3, 2, 64, 256
     r = np.random.default_rng(27)
