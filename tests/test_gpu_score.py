@@ -73,7 +73,7 @@ def check(seed, B, Hq, Hkv, N, d, dtype="bf16", ranges=None, slopes=False, cap=0
     gl = lse.double().cpu().numpy()
     assert np.array_equal(np.isneginf(gl), np.isneginf(rl))
     fin = np.isfinite(rl)
-    assert (np.abs(gl - rl)[fin] <= (dx * math.log(2) + 2.0 ** -20 * (1 + np.abs(rl)))[fin]).all()
+    assert (np.abs(gl[fin] - rl[fin]) <= dx[fin] * math.log(2) + 2.0 ** -20 * (1 + np.abs(rl[fin]))).all()
     if not backward:
         return
     got = run_bwd(*dev[:3], o, lse, dev[3], *mods)
