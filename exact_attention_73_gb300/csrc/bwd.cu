@@ -170,17 +170,11 @@ cudaError_t launch_main_dt(int dt, int hd, const CUtensorMap& k, const CUtensorM
 template <typename T, int D>
 static cudaError_t launch_pre(const void* o, const void* dout, float* dvec, float* dq_acc, long long rows, int Hq,
                               int T_tokens, int packed, cudaStream_t st, bool beside) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = beside ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, bwd_pre_kernel<T, D>, static_cast<const T*>(o), static_cast<const T*>(dout), dvec,
-                            dq_acc, rows, Hq, T_tokens, packed);
+  const dim3 grid(static_cast<unsigned>((rows + 7) / 8));
+  const T *x = static_cast<const T*>(o), *y = static_cast<const T*>(dout);
+  if (beside) return launch_dependent(bwd_pre_kernel<T, D>, grid, 256, 0, st, x, y, dvec, dq_acc, rows, Hq, T_tokens, packed);
+  bwd_pre_kernel<T, D><<<grid, 256, 0, st>>>(x, y, dvec, dq_acc, rows, Hq, T_tokens, packed);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_bwd_pre(int dt, int d, const void* o, const void* dout, float* dvec, float* dq_acc, long long rows,

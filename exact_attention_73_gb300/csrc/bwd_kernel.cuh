@@ -214,7 +214,9 @@ __device__ __forceinline__ uint32_t transpose_bits(uint32_t x, int lane) {
 // from the capped score itself. Row masks: lane e of a warp holds query e's
 // visible keys as a bit for each of the warp's 32 keys; if any bit is
 // missing the 32 x 32 bits are transposed across the warp, so that each lane
-// has its own key's bit for every query.
+// has its own key's bit for every query. B = 1, Hq = 32, Hkv = 8, N = 8192, d =
+// 128, causal, bf16: cap 1625 us (845 TFLOP/s), bias 1540, both 1805, ranges
+// alone 1445, the plain kernel 1390, whose bounds these share.
 template <int DT, int D, bool kDQ = true, bool kSplit = false, bool kPersist = false, int kScore = 0>
 __global__ void __launch_bounds__(512, 1)
 bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,

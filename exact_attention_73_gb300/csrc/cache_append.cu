@@ -15,6 +15,12 @@
 // latency-bound for single tokens, where the earlier rows' codes (at most 16
 // KB at d = 128) are read for their largest magnitude: E4M3 magnitudes order
 // as their low seven bits, so that maximum is taken on packed bytes.
+//
+// Measured (L2 flushed, d = 128, 8 KV heads): one token of 64 sequences 10 us;
+// 4000 rows of 8 sequences 41 us without rotation, 4.8 TB/s, 57 with 64 of the
+// keys' 128 elements turned (the rotation is made twice, for the largest
+// magnitude and for the codes). Heads of a block side by side in the launch
+// order, more unrolling, or 256 threads changed neither by more than 4 %.
 #include <cstdint>
 
 #include "../../include/libattn.h"

@@ -24,15 +24,18 @@
 // (a power of two: BF16's 8 and FP16's 11 bits stay exact).
 //
 // The work is the visible 128-key blocks of all items (8 or 16 heads of a KV
-// head of a sequence), laid end to end; the grid fills the GPU once and every
-// CTA takes an equal run of blocks, whatever the lengths: a run may cover
-// parts of several items, an item may be cut into pieces (short runs: one
-// piece of one item each). (A fixed number of
-// pieces per item, each a CTA, leaves a part of a wave idle: 16 caches of
-// 32768 tokens took 186 to 266 us depending on that number, ragged lengths
-// 33 to 98 us.) A CTA's four warps take every fourth 64 keys of a piece
-// and meet once, at its end. A second kernel combines the pieces of an item
-// by their log-sum-exp weights.
+// head of a sequence); the grid fills the GPU once and the blocks are dealt to
+// its CTAs by the lengths (decode_cache_kernel): as one piece of an item each,
+// or as equal runs of all blocks laid end to end. (A fixed number of pieces
+// per item, each a CTA, leaves a part of a wave idle: 16 caches of 32768
+// tokens took 186 to 266 us depending on that number, ragged lengths 33 to 98
+// us.) A CTA's four warps take every fourth 64 keys of a piece and meet once,
+// at its end. A second kernel combines the pieces of an item by their
+// log-sum-exp weights.
+//
+// Measured (L2 flushed, d = 128): 16 caches of 32768 tokens, 8 KV heads, bf16
+// 165 us, 6.5 TB/s, 0.96 of the copy bandwidth; 37 paged caches of 0 to 4500
+// tokens, 4 KV heads, cap and bias 33 us.
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -50,7 +53,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTau = 8.f;      // the running max is left behind by up to this (log2 units)
-constexpr int kEvenRun = 16;     // blocks per CTA from which runs are cut without regard to items
+constexpr int kEvenRun = 16;     // blocks per CTA from which runs may be cut without regard to items
 constexpr float kPShift = 7.f;   // P~ = 2^7 exp2(x - m) <= 2^15
 
 struct CacheDecArgs {
@@ -154,10 +157,10 @@ __device__ __forceinline__ long long cta_sum(long long x, long long* scratch) {
   return x;
 }
 
-// Blocks blk0 .. blk1 - 1 of one item: `piece` of `pieces`.
+// Blocks blk0 .. blk1 - 1 of one item: piece_of.x of piece_of.y (in shared memory).
 template <typename T, int D, int NR>
 __device__ __forceinline__ void decode_piece(const CacheDecArgs& a, float* smem, int b, int h, int rg, int lo, int L,
-                                             int blk0, int blk1, int piece, int pieces) {
+                                             int blk0, int blk1, const volatile int2* piece_of) {
   constexpr int NG = D / 64;                     // 64-dim groups of the K contraction
   constexpr int VB = D == 64 ? 8 : 16;           // bytes of a V row per lane and half
   constexpr int NH = D == 256 ? 2 : 1;           // halves of a V row
@@ -520,6 +523,7 @@ __device__ __forceinline__ void decode_piece(const CacheDecArgs& a, float* smem,
       }
     }
   __syncthreads();
+  const int piece = piece_of->x, pieces = piece_of->y;
   for (int i = threadIdx.x; i < heads * (D / 2); i += 32 * kWarps) {
     const int col = i / (D / 2), dim = 2 * (i % (D / 2));
     float mx = -INFINITY;
@@ -555,47 +559,90 @@ decode_cache_kernel(const CacheDecArgs a) {
   extern __shared__ float smem[];                // [kWarps][8 NR][D] partial O, then m and l
   __shared__ long long sh_scan[kWarps], sh_start;
   __shared__ int sh_b;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // what is carried from piece to piece: here and not in registers, which the pieces need
+  __shared__ struct {
+    long long at, end, quota, before;
+    int way, size, b0;
+    int2 piece;
+    int n[32 * kWarps];       // blocks of sequence threadIdx.x of the 128 looked at
+  } plan;
+  const int lane = threadIdx.x & 31;
   const int per_seq = a.Hkv * a.row_groups;      // items per sequence
   // `at`: where this CTA stands, in units of the way the work is dealt.
-  // kWhole (one split): items, round-robin. kCut: blocks of the total, an even
-  // run per CTA wherever items begin. kPieces, for short runs, where a second
-  // piece would cost a CTA more than it evens out: pieces of at most `size`
-  // blocks, the smallest size that needs no more CTAs than there are.
+  // kWhole (one split): items, round-robin.
+  // kPieces: pieces of at most `size` blocks, the smallest size that needs no
+  // more CTAs than there are. Short runs of blocks, and ragged lengths where
+  // nearly all CTAs then have a piece.
+  // kCut: blocks of the total, an even run per CTA wherever items begin. Where
+  // equal lengths leave a part of the CTAs without a piece; a second piece
+  // costs a CTA its set-up.
+  // 16 caches of 32768 tokens and 8 heads 176 us cut, 184 in pieces; 64 of 2048
+  // 59 and 76; with ragged lengths up to these 118 and 110, 59 and 55.
   enum { kWhole, kCut, kPieces };
-  int way = kWhole, size = 1;
-  int n = 0;                  // blocks of sequence threadIdx.x of the 128 looked at
-  long long at = blockIdx.x, end = static_cast<long long>(a.B) * per_seq, quota = 1;
-  if (a.splits > 1) {
+  if (a.splits == 1) {
+    if (threadIdx.x == 0) {
+      plan.way = kWhole;
+      plan.at = blockIdx.x;
+      plan.end = static_cast<long long>(a.B) * per_seq;
+    }
+  } else {
     grid_launch_dependents();   // the combine kernel may be set up
-    long long total = 0;
-    for (int b = threadIdx.x; b < a.B; b += 32 * kWarps) total += n = visible_blocks(visible_keys(a, b));
+    int way, size = 1;
+    long long at = blockIdx.x, end = LLONG_MAX, quota = 1, total = 0;
+    const int n0 = visible_blocks(visible_keys(a, 0));
+    int n = 0;
+    bool same = true;           // all sequences have as many blocks
+    for (int b = threadIdx.x; b < a.B; b += 32 * kWarps) {
+      total += n = visible_blocks(visible_keys(a, b));
+      same = same && n == n0;
+    }
     total = cta_sum(total, sh_scan) * per_seq;
     const long long even = (total + gridDim.x - 1) / gridDim.x;   // blocks per CTA
-    if (even >= kEvenRun) {
-      way = kCut;
-      quota = max(even, static_cast<long long>(a.min_quota));
-      at = blockIdx.x * quota;
-      end = min(at + quota, total);
-    } else {
-      way = kPieces;
-      end = LLONG_MAX;
+    way = even >= kEvenRun && __syncthreads_and(same) ? kCut : kPieces;
+    if (way == kPieces) {
       size = max(a.min_quota, 1);
       int hi = max(size, a.blocks);   // whole items
+      long long count = 0;            // pieces of `hi` blocks, once it has come down
       while (size < hi) {
         const int mid = (size + hi) >> 1;
         long long c = 0;
         if (a.B <= 32 * kWarps) c = (n + mid - 1) / mid;
         else
           for (int b = threadIdx.x; b < a.B; b += 32 * kWarps) c += (visible_blocks(visible_keys(a, b)) + mid - 1) / mid;
-        if (cta_sum(c, sh_scan) * per_seq <= gridDim.x) hi = mid;
-        else size = mid + 1;
+        c = cta_sum(c, sh_scan) * per_seq;
+        if (c <= gridDim.x) {
+          hi = mid;
+          count = c;
+        } else {
+          size = mid + 1;
+        }
       }
+      if (even >= kEvenRun && 10 * count < 9LL * gridDim.x) way = kCut;   // too few, or more than CTAs even whole
+    }
+    if (way == kCut) {
+      quota = max(even, static_cast<long long>(a.min_quota));
+      at = blockIdx.x * quota;
+      end = min(at + quota, total);
+    }
+    plan.n[threadIdx.x] = n;
+    if (threadIdx.x == 0) {
+      plan.way = way;
+      plan.at = at;
+      plan.end = end;
+      plan.quota = quota;
+      plan.size = size;
+      plan.b0 = 0;
+      plan.before = 0;
     }
   }
-  int b0 = 0;                 // the sequences looked at: b0 .. b0 + 127
-  long long before = 0;       // weight of those before: blocks (kCut) or pieces of an item (kPieces)
-  for (; at < end; __syncthreads()) {   // smem is the next piece's
+  while (true) {
+    __syncthreads();          // the plan stands, and smem is this piece's
+    const int way = plan.way, size = plan.size;
+    const long long end = plan.end, quota = plan.quota;
+    long long at = plan.at;
+    int b0 = plan.b0;         // the sequences looked at: b0 .. b0 + 127
+    long long before = plan.before;   // weight of those before: blocks (kCut) or pieces of an item (kPieces)
+    if (at >= end) return;
     int b, i, piece = 0, pieces = 1, blk0, blk1;
     int2 k;
     if (way == kWhole) {
@@ -609,6 +656,7 @@ decode_cache_kernel(const CacheDecArgs a) {
       // the sequence that `at` lies in
       if (threadIdx.x == 0) sh_b = -1;
       while (true) {
+        int n = plan.n[threadIdx.x];
         if (a.B > 32 * kWarps)
           n = b0 + static_cast<int>(threadIdx.x) < a.B ? visible_blocks(visible_keys(a, b0 + threadIdx.x)) : 0;
         const int wt = way == kCut ? n : (n + size - 1) / size;
@@ -619,11 +667,11 @@ decode_cache_kernel(const CacheDecArgs a) {
           if (lane >= o) incl += y;
         }
         __syncthreads();      // sh_scan was read, sh_b is set
-        if (lane == 31) sh_scan[warp] = incl;
+        if (lane == 31) sh_scan[threadIdx.x >> 5] = incl;
         __syncthreads();
         long long first = before + incl - wt, all = 0;
         for (int w = 0; w < kWarps; ++w) {
-          if (w < warp) first += sh_scan[w];
+          if (w < static_cast<int>(threadIdx.x >> 5)) first += sh_scan[w];
           all += sh_scan[w];
         }
         if (wt > 0 && at >= first * per_seq && at < (first + wt) * per_seq) {
@@ -661,9 +709,16 @@ decode_cache_kernel(const CacheDecArgs a) {
       }
       if (piece == 0 && threadIdx.x == 0) a.pieces[static_cast<long long>(b) * per_seq + i] = pieces;
     }
+    __syncthreads();          // the plan was read
+    if (threadIdx.x == 0) {
+      plan.at = at;
+      plan.b0 = b0;
+      plan.before = before;
+      plan.piece = make_int2(piece, pieces);
+    }
     const int h = i / a.row_groups, rg = i % a.row_groups;
     if (blk0 < blk1) {
-      decode_piece<T, D, NR>(a, smem, b, h, rg, k.x, k.y, blk0, blk1, piece, pieces);
+      decode_piece<T, D, NR>(a, smem, b, h, rg, k.x, k.y, blk0, blk1, &plan.piece);
     } else if (way == kWhole) {   // a sequence without keys
       const int head0 = rg * 8 * NR, heads = min(a.group - head0, 8 * NR);
       const long long row = static_cast<long long>(b) * a.Hq + static_cast<long long>(h) * a.group + head0;
@@ -775,19 +830,10 @@ cudaError_t launch_decode(const CacheDecArgs& a, cudaStream_t st) {
   decode_cache_kernel<T, D, NR><<<static_cast<unsigned>(most < places ? most : places), 32 * kWarps, SMEM, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
   // a programmatic dependent: its launch overlaps the pieces' kernel, whose results it waits for
-  cudaLaunchConfig_t cfg = {};
   const long long rows = static_cast<long long>(a.B) * a.Hq;
-  const bool few = rows <= 4 * sms;   // eight warps a row still fit at once
-  cfg.gridDim = dim3(static_cast<unsigned>(few ? rows : (rows + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, combine_kernel<T, D, NR, 8>, a)
-             : cudaLaunchKernelEx(&cfg, combine_kernel<T, D, NR, 1>, a);
+  if (rows <= 4 * sms)   // eight warps a row still fit at once
+    return launch_dependent(combine_kernel<T, D, NR, 8>, dim3(static_cast<unsigned>(rows)), 256, 0, st, a);
+  return launch_dependent(combine_kernel<T, D, NR, 1>, dim3(static_cast<unsigned>((rows + 7) / 8)), 256, 0, st, a);
 }
 
 template <typename T>

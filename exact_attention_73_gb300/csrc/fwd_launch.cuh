@@ -39,17 +39,7 @@ cudaError_t launch_fwd_grid(const CUtensorMap& q, const CUtensorMap& k, const CU
     if (grid > sms) grid = sms;
   }
   if constexpr ((kScore & kScoreRanges) != 0) {   // its set-up overlaps the tile facts' kernel
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(R::NTHREADS);
-    cfg.dynamicSmemBytes = R::SMEM_BYTES;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, q, k, v, u);
+    return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), R::NTHREADS, R::SMEM_BYTES, st, q, k, v, u);
   } else {
     kern<<<static_cast<unsigned>(grid), R::NTHREADS, R::SMEM_BYTES, st>>>(q, k, v, u);
     return cudaGetLastError();

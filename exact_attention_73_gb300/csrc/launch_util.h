@@ -21,6 +21,24 @@ cudaError_t smem_attr_once(int bytes) {
   return e;
 }
 
+// Launches `kern` as a programmatic dependent: its CTAs may start once those
+// of the launch before it have all started and said so (grid_launch_dependents)
+// or ended; what it needs of that launch it waits for (grid_wait_prerequisites).
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // Checks once that kernel Kern is built with at least `regs` registers per
 // thread for blocks of `threads`: a register split by role (setmaxnreg)
 // hands out the registers the block was launched with, and a split larger

@@ -21,6 +21,10 @@
 // the rest, within an eighth of a turn, are polynomials (minimax, fitted by
 // the Remez exchange; 9e-8 with their FP32 evaluation). HBM-bound: 8 bytes out
 // per pair.
+//
+// Measured (L2 flushed): gradients of B = 2, H = 32, N = 8192, d = 128 from
+// dense to token-major rows 44.5 us, 6.1 TB/s; tables of 131072 positions of
+// 64 pairs 16.4 us where filling the same bytes with a constant takes 14.3.
 #include <climits>
 #include <cstdint>
 
@@ -134,9 +138,10 @@ template <typename T, int D, bool kInterleaved>
 cudaError_t launch_rope_heads(const RopeArgs& a, cudaStream_t st) {
   constexpr int ROWS = 256 / (D / 16);
   const long long gx = (a.rows + ROWS - 1) / ROWS;
-  // one head per thread while that still leaves every SM few warps (single
-  // tokens: latency), else eight heads per table entry
-  const bool few = gx * ((a.H + 7) / 8) < 2 * 152;
+  // one head per thread while eight would leave SMs without a block (latency:
+  // 64 tokens of 32 heads 6.1 against 8.2 us), else eight per table entry (one
+  // row of 2048 x 32 heads x 128 10.2 against 12.3 us)
+  const bool few = gx * ((a.H + 7) / 8) < 152;
   const int per = few ? 1 : 8;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>((a.H + per - 1) / per));
   if (few) rope_kernel<T, D, kInterleaved, 1><<<grid, 256, 0, st>>>(a);

@@ -12,9 +12,11 @@
 // KV range. Per 128 keys the 64-row tiles that see one of them: the
 // backward's walk. From these the order of the units, most work first (a
 // counting sort): with documents the work of neighbouring tiles differs by
-// their length, and a long one started last would run alone. The kernel behind
-// them is a programmatic dependent: the forward sets itself up meanwhile, and
-// the backward's row sums, which need no facts, run beside them.
+// their length, and a long one started last would run alone. These kernels are
+// short and bound by latency, so each is a programmatic dependent of the one
+// before it, and so is the kernel behind them: the forward sets itself up
+// meanwhile, and the backward's row sums, which need no facts, run beside them
+// (12 documents in 16384 rows, 16 heads, d = 64: 209 -> 196 us).
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -135,9 +137,8 @@ __global__ void __launch_bounds__(256) mask_rows_kernel(const int* __restrict__ 
   }
 }
 
-// Union of the visible keys of a 64-row tile, by one warp: a lane's two rows
-// (tile i of sequence b), then over the lanes.
-__device__ __forceinline__ int2 tile_rows(const int2* ranges, int b, int i, int N, int left, int right, int lane) {
+// Union of the visible keys of 64-row tile i of sequence b, by one warp.
+__device__ __forceinline__ int2 tile_bounds(const int2* ranges, int b, int i, int N, int left, int right, int lane) {
   int2 v = make_int2(N, 0);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
@@ -147,9 +148,6 @@ __device__ __forceinline__ int2 tile_rows(const int2* ranges, int b, int i, int 
     v.x = min(v.x, s.x);
     v.y = max(v.y, s.y);
   }
-  return v;
-}
-__device__ __forceinline__ int2 tile_union(int2 v) {
   return make_int2(__reduce_min_sync(0xffffffffu, v.x), __reduce_max_sync(0xffffffffu, v.y));
 }
 // The 64-row tiles of a sequence (bounds) with a row that may see one of keys 128j .., by one warp.
@@ -175,15 +173,17 @@ __device__ __forceinline__ int2 tiles_of_keys(const int2* bounds, int j, int nti
 __global__ void __launch_bounds__(256) score_bounds_kernel(const int2* __restrict__ ranges, int2* __restrict__ bounds,
                                                            int N, int ntile, int left, int right) {
   const int i = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, b = blockIdx.y;
+  grid_launch_dependents();
   if (i >= ntile) return;
-  const int2 v = tile_union(tile_rows(ranges, b, i, N, left, right, lane));
+  const int2 v = tile_bounds(ranges, b, i, N, left, right, lane);
   if (lane == 0) bounds[static_cast<long long>(b) * ntile + i] = v;
 }
 
 // One warp per 128 keys.
-__global__ void __launch_bounds__(256) score_key_tiles_kernel(const int2* __restrict__ bounds, int2* __restrict__ key_tiles,
-                                                              int ntile, int nkey) {
+__global__ void __launch_bounds__(256) score_key_tiles_kernel(const int2* bounds, int2* key_tiles, int ntile, int nkey) {
   const int j = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, b = blockIdx.y;
+  grid_launch_dependents();
+  grid_wait_prerequisites();   // every CTA: who waits for this grid waits for the bounds too
   if (j >= nkey) return;
   const int2 v = tiles_of_keys(bounds + static_cast<long long>(b) * ntile, j, ntile, lane);
   if (lane == 0) key_tiles[static_cast<long long>(b) * nkey + j] = v;
@@ -249,31 +249,24 @@ __global__ void __launch_bounds__(kBins) score_order_kernel(const int2* facts, i
                                                             int ntile, int most) {
   __shared__ OrderSmem sm;
   grid_launch_dependents();
+  grid_wait_prerequisites();
   sort_units<long long>(sm, facts, order, B, nx, group, ntile, most);
 }
 
 // Few rows: bounds, key tiles (nkey > 0) and order by one CTA, in place of
-// two or three launches.
-constexpr int kFactsRows = 16384;
+// two or three launches (1024 rows, forward and backward of one head at d =
+// 64: 16.4 and 23.6 us against 17.4 and 25.6; 4096 rows 18.4 and 27.6 against
+// 17.4 and 27.6, 16384 rows 24.6 and 37.9 against the same).
+constexpr int kFactsRows = 2048;
 __global__ void __launch_bounds__(kBins) score_facts_kernel(const int2* __restrict__ ranges, int2* bounds,
                                                             int2* key_tiles, int2* order, int B, int N, int ntile,
                                                             int nkey, int nx, int group, int left, int right) {
   __shared__ OrderSmem sm;
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int U = 4;   // tiles of a warp whose loads are in flight together
-  for (int u0 = warp; u0 < B * ntile; u0 += 32 * U) {
-    int2 v[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int u = u0 + 32 * k;
-      v[k] = u < B * ntile ? tile_rows(ranges, u / ntile, u % ntile, N, left, right, lane) : make_int2(N, 0);
-    }
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      v[k] = tile_union(v[k]);
-      if (lane == 0 && u0 + 32 * k < B * ntile) bounds[u0 + 32 * k] = v[k];
-    }
+  for (int u = warp; u < B * ntile; u += 32) {
+    const int2 v = tile_bounds(ranges, u / ntile, u % ntile, N, left, right, lane);
+    if (lane == 0) bounds[u] = v;
   }
   __syncthreads();
   for (int u = warp; u < B * nkey; u += 32) {
@@ -322,15 +315,13 @@ cudaError_t prepare_score(ScoreArgs& a, const int* row_ranges, const float* slop
   score_bounds_kernel<<<dim3((a.ntile + 7) / 8, B), 256, 0, st>>>(a.ranges, bounds, N, a.ntile, left, right);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (keys) {
-    score_key_tiles_kernel<<<dim3((nkeys(N) + 7) / 8, B), 256, 0, st>>>(bounds, kt, a.ntile, nkeys(N));
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    score_order_kernel<<<1, kBins, 0, st>>>(kt, order, B, nkeys(N), 0, a.ntile, a.ntile);
-  } else {
-    score_order_kernel<<<1, kBins, 0, st>>>(bounds, order, B, (N + unit_rows - 1) / unit_rows, unit_rows / 64, a.ntile,
-                                            nkeys(N));
-  }
-  return cudaGetLastError();
+  if (!keys)
+    return launch_dependent(score_order_kernel, dim3(1), kBins, 0, st, bounds, order, B, (N + unit_rows - 1) / unit_rows,
+                            unit_rows / 64, a.ntile, nkeys(N));
+  if ((e = launch_dependent(score_key_tiles_kernel, dim3((nkeys(N) + 7) / 8, B), 256, 0, st, bounds, kt, a.ntile,
+                            nkeys(N))) != cudaSuccess)
+    return e;
+  return launch_dependent(score_order_kernel, dim3(1), kBins, 0, st, kt, order, B, nkeys(N), 0, a.ntile, a.ntile);
 }
 
 int score_mode(const int* row_ranges, const float* slopes, float cap) {
