@@ -89,7 +89,9 @@ struct BwdArgs {
   // persistent instance: the grid walks units blockIdx.x, + gridDim.x, ...
   // below `units` (tiles_x * Hkv * batch), in the linear order above
   int units;
-  ScoreArgs sc;                 // kScore instances only
+};
+struct BwdScoreArgs : BwdArgs {   // kScore instances
+  ScoreArgs sc;
 };
 
 // kP: the persistent walk's layout. At d = 64 it holds two K/V buffers, so
@@ -215,13 +217,14 @@ __device__ __forceinline__ uint32_t transpose_bits(uint32_t x, int lane) {
 // visible keys as a bit for each of the warp's 32 keys; if any bit is
 // missing the 32 x 32 bits are transposed across the warp, so that each lane
 // has its own key's bit for every query. B = 1, Hq = 32, Hkv = 8, N = 8192, d =
-// 128, causal, bf16: cap 1625 us (845 TFLOP/s), bias 1540, both 1805, ranges
-// alone 1445, the plain kernel 1390, whose bounds these share.
+// 128, causal, bf16: cap 1594 us (862 TFLOP/s), bias 1524, both 1778, ranges
+// alone 1433, the plain kernel 1363, whose bounds these share.
 template <int DT, int D, bool kDQ = true, bool kSplit = false, bool kPersist = false, int kScore = 0>
 __global__ void __launch_bounds__(512, 1)
 bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
            const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
-           const __grid_constant__ CUtensorMap tmdQ, const BwdArgs a) {
+           const __grid_constant__ CUtensorMap tmdQ,
+           const std::conditional_t<kScore != 0, BwdScoreArgs, BwdArgs> a) {
   using C = BwdCfg<DT, D, kPersist>;
   static_assert(!kPersist || (!kSplit && C::DSPLIT == 1), "persistent walk: whole units, one CTA per key tile");
   // The layout uses all the shared memory it asks for, with no room to align
@@ -492,7 +495,11 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     // -------------------------------------------------------------- MMA
     // Order: SdP(0); per iteration it: SdP(it+1) into the other buffer, then
     // (after P^T/dS^T of it are ready) the two dQ^T halves, dV and dK of it.
-    if (elect_one()) {
+    // (elect_one, but for the plain kernel at d = 256: 5126 us by lane, 5449
+    // elected, B = 2, H = 8, N = 8192; with a cap and ranges 1513 and 1420, 1295
+    // and 1218, B = 1, causal)
+    constexpr bool kElect = D != 256 || kScore != 0;
+    if (kElect ? elect_one() : lane == 0) {
       // Descriptors are built once; a byte offset is added to the
       // start-address field (16-byte units) for each K step and stage.
       const uint64_t dK_kmaj = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128);
@@ -798,64 +805,60 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
           }
         }
         uint32_t pp[16], dd[16];
-        auto weights = [&](auto raw_scores) {
-          [[maybe_unused]] constexpr bool kRaw = decltype(raw_scores)::value;
   #pragma unroll
-        for (int e4 = 0; e4 < 8; ++e4) {
-          const float4 l4 = l4r[e4];
-          const float4 d4 = d4r[e4];
-          float2 s01 = make_float2(__uint_as_float(sv[4 * e4]), __uint_as_float(sv[4 * e4 + 1]));
-          float2 s23 = make_float2(__uint_as_float(sv[4 * e4 + 2]), __uint_as_float(sv[4 * e4 + 3]));
-          float2 x01, x23;
-          if constexpr (kCap) {
-            if constexpr (kRaw) {
-              s01 = fmul2(s01, cap_small_factor(s01, a.sc));
-              s23 = fmul2(s23, cap_small_factor(s23, a.sc));
+        for (int way = 0; way < (kCap ? 2 : 1); ++way) {   // capped: raw scores, or capped already
+          [[maybe_unused]] const bool kRaw = way == 0;
+          if (kCap && raw != kRaw) continue;
+    #pragma unroll
+          for (int e4 = 0; e4 < 8; ++e4) {
+            const float4 l4 = l4r[e4];
+            const float4 d4 = d4r[e4];
+            float2 s01 = make_float2(__uint_as_float(sv[4 * e4]), __uint_as_float(sv[4 * e4 + 1]));
+            float2 s23 = make_float2(__uint_as_float(sv[4 * e4 + 2]), __uint_as_float(sv[4 * e4 + 3]));
+            float2 x01, x23;
+            if constexpr (kCap) {
+              if (kRaw) {
+                s01 = fmul2(s01, cap_small_factor(s01, a.sc));
+                s23 = fmul2(s23, cap_small_factor(s23, a.sc));
+              }
+              x01 = fadd2(s01, make_float2(l4.x, l4.y));
+              x23 = fadd2(s23, make_float2(l4.z, l4.w));
+            } else {
+              x01 = ffma2(s01, sl2v, make_float2(l4.x, l4.y));
+              x23 = ffma2(s23, sl2v, make_float2(l4.z, l4.w));
             }
-            x01 = fadd2(s01, make_float2(l4.x, l4.y));
-            x23 = fadd2(s23, make_float2(l4.z, l4.w));
-          } else {
-            x01 = ffma2(s01, sl2v, make_float2(l4.x, l4.y));
-            x23 = ffma2(s23, sl2v, make_float2(l4.z, l4.w));
-          }
-          float p[4] = {ex2(x01.x), ex2(x01.y), ex2(x23.x), ex2(x23.y)};
-          if (kScore == 0 && edge) {
-  #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int q = q0 + 4 * e4 + u;
-              if (!kvalid || (a.win_right >= 0 && kloc > q + a.win_right) || (a.win_left >= 0 && kloc < q - a.win_left))
-                p[u] = 0.f;
+            float p[4] = {ex2(x01.x), ex2(x01.y), ex2(x23.x), ex2(x23.y)};
+            if (kScore == 0 && edge) {
+    #pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int q = q0 + 4 * e4 + u;
+                if (!kvalid || (a.win_right >= 0 && kloc > q + a.win_right) || (a.win_left >= 0 && kloc < q - a.win_left))
+                  p[u] = 0.f;
+              }
+            }
+            const float2 t01 = fadd2(make_float2(__uint_as_float(dp[4 * e4]), __uint_as_float(dp[4 * e4 + 1])),
+                                     make_float2(d4.x, d4.y));
+            const float2 t23 = fadd2(make_float2(__uint_as_float(dp[4 * e4 + 2]), __uint_as_float(dp[4 * e4 + 3])),
+                                     make_float2(d4.z, d4.w));
+            float2 g01 = fmul2(make_float2(p[0], p[1]), t01);
+            float2 g23 = fmul2(make_float2(p[2], p[3]), t23);
+            if constexpr (kCap) {   // 1 - tanh^2
+              const float2 c2 = make_float2(a.sc.neg_inv_cap2_sq, a.sc.neg_inv_cap2_sq), one = make_float2(1.f, 1.f);
+              g01 = fmul2(g01, ffma2(fmul2(s01, s01), c2, one));
+              g23 = fmul2(g23, ffma2(fmul2(s23, s23), c2, one));
+            }
+            if constexpr (DT == kBF16) {
+              pp[2 * e4] = pack_bf16x2(p[0], p[1]);
+              pp[2 * e4 + 1] = pack_bf16x2(p[2], p[3]);
+              dd[2 * e4] = pack_bf16x2(g01.x, g01.y);
+              dd[2 * e4 + 1] = pack_bf16x2(g23.x, g23.y);
+            } else {
+              pp[2 * e4] = pack_f16x2(p[0], p[1]);
+              pp[2 * e4 + 1] = pack_f16x2(p[2], p[3]);
+              dd[2 * e4] = pack_f16x2(g01.x, g01.y);
+              dd[2 * e4 + 1] = pack_f16x2(g23.x, g23.y);
             }
           }
-          const float2 t01 = fadd2(make_float2(__uint_as_float(dp[4 * e4]), __uint_as_float(dp[4 * e4 + 1])),
-                                   make_float2(d4.x, d4.y));
-          const float2 t23 = fadd2(make_float2(__uint_as_float(dp[4 * e4 + 2]), __uint_as_float(dp[4 * e4 + 3])),
-                                   make_float2(d4.z, d4.w));
-          float2 g01 = fmul2(make_float2(p[0], p[1]), t01);
-          float2 g23 = fmul2(make_float2(p[2], p[3]), t23);
-          if constexpr (kCap) {   // 1 - tanh^2
-            const float2 c2 = make_float2(a.sc.neg_inv_cap2_sq, a.sc.neg_inv_cap2_sq), one = make_float2(1.f, 1.f);
-            g01 = fmul2(g01, ffma2(fmul2(s01, s01), c2, one));
-            g23 = fmul2(g23, ffma2(fmul2(s23, s23), c2, one));
-          }
-          if constexpr (DT == kBF16) {
-            pp[2 * e4] = pack_bf16x2(p[0], p[1]);
-            pp[2 * e4 + 1] = pack_bf16x2(p[2], p[3]);
-            dd[2 * e4] = pack_bf16x2(g01.x, g01.y);
-            dd[2 * e4 + 1] = pack_bf16x2(g23.x, g23.y);
-          } else {
-            pp[2 * e4] = pack_f16x2(p[0], p[1]);
-            pp[2 * e4 + 1] = pack_f16x2(p[2], p[3]);
-            dd[2 * e4] = pack_f16x2(g01.x, g01.y);
-            dd[2 * e4 + 1] = pack_f16x2(g23.x, g23.y);
-          }
-        }
-        };
-        if constexpr (kCap) {
-          if (raw) weights(std::true_type{});
-          else weights(std::false_type{});
-        } else {
-          weights(std::true_type{});
         }
         tmem_st16(xb + C::col_p(2 * half), pp);
         tmem_st16(xb + C::col_ds(2 * half), dd);

@@ -1,4 +1,4 @@
-// Launch of the backward's score-modified instances (BwdArgs::sc set): whole
+// Launch of the backward's score-modified instances (BwdScoreArgs): whole
 // units, one CTA per key tile (two at d = 256).
 #pragma once
 #include "bwd_kernel.cuh"
@@ -8,7 +8,7 @@ namespace attn {
 
 template <int DT, int D, int kScore>
 cudaError_t launch_bwd_score_inst(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
-                                  const CUtensorMap& d, const CUtensorMap& dq, const BwdArgs& a, int N, int nz,
+                                  const CUtensorMap& d, const CUtensorMap& dq, const BwdScoreArgs& a, int N, int nz,
                                   cudaStream_t st) {
   using C = BwdCfg<DT, D>;
   cudaError_t e = smem_attr_once<bwd_kernel<DT, D, true, false, false, kScore>>(C::SMEM_BYTES);
@@ -17,7 +17,7 @@ cudaError_t launch_bwd_score_inst(const CUtensorMap& k, const CUtensorMap& v, co
     return e;
   const dim3 grid(static_cast<unsigned>((N + C::BC - 1) / C::BC * C::DSPLIT), static_cast<unsigned>(a.Hkv),
                   static_cast<unsigned>(nz));
-  BwdArgs g = a;
+  BwdScoreArgs g = a;
   g.tiles_x = 0;
   g.unit0 = 0;
   g.nsplit = 1;
@@ -28,7 +28,7 @@ cudaError_t launch_bwd_score_inst(const CUtensorMap& k, const CUtensorMap& v, co
 // mode: kScoreCap, kScoreBias, kScoreRanges together, not 0
 template <int DT, int D>
 cudaError_t launch_bwd_score_mode(int mode, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
-                                  const CUtensorMap& d, const CUtensorMap& dq, const BwdArgs& a, int N, int nz,
+                                  const CUtensorMap& d, const CUtensorMap& dq, const BwdScoreArgs& a, int N, int nz,
                                   cudaStream_t st) {
   switch (mode) {
     case 1: return launch_bwd_score_inst<DT, D, 1>(k, v, q, d, dq, a, N, nz, st);

@@ -24,6 +24,7 @@ attn_status bwd_check_dense(const void* q, const void* k, const void* v, const v
                             size_t ws_bytes, int B, int Hq, int Hkv, int N, int d, attn_dtype dtype);
 
 struct BwdArgs;
+struct BwdScoreArgs;
 bool operand_map(CUtensorMap* m, const void* base, int dt, int d, bool packed, int B, int H, long long rows,
                  int box_rows);
 cudaError_t launch_bwd_pre(int dt, int d, const void* o, const void* dout, float* dvec, float* dq_acc,
@@ -38,15 +39,15 @@ bool accum_map(CUtensorMap* m, const float* base, int d, bool packed, int B, int
 // (the box of its map).
 int bwd_dq_rows(int d);
 int bwd_dq_dims(int d);
-// Score-modified main kernels (BwdArgs::sc set; mode: what they change), dense.
+// Score-modified main kernels (mode: what they change), dense.
 cudaError_t launch_bwd_score_64(int mode, int dt, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
-                                const CUtensorMap& dout, const CUtensorMap& dq_acc, const BwdArgs& a, int N, int nz,
+                                const CUtensorMap& dout, const CUtensorMap& dq_acc, const BwdScoreArgs& a, int N, int nz,
                                 cudaStream_t st);
 cudaError_t launch_bwd_score_128(int mode, int dt, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
-                                 const CUtensorMap& dout, const CUtensorMap& dq_acc, const BwdArgs& a, int N, int nz,
+                                 const CUtensorMap& dout, const CUtensorMap& dq_acc, const BwdScoreArgs& a, int N, int nz,
                                  cudaStream_t st);
 cudaError_t launch_bwd_score_256(int mode, int dt, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
-                                 const CUtensorMap& dout, const CUtensorMap& dq_acc, const BwdArgs& a, int N, int nz,
+                                 const CUtensorMap& dout, const CUtensorMap& dq_acc, const BwdScoreArgs& a, int N, int nz,
                                  cudaStream_t st);
 cudaError_t launch_bwd_dkdv(int dt, int d, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
                             const CUtensorMap& dout, const BwdArgs& a, int max_len, int nz, cudaStream_t st);

@@ -439,7 +439,7 @@ extern "C" attn_status attn_bwd_score(const void* q, const void* k, const void* 
       !operand_map(&tq, q, dtype, d, false, B, Hq, N, 64) || !operand_map(&tdo, dout, dtype, d, false, B, Hq, N, 64) ||
       !accum_map(&tdq, dq_acc, d, false, B, Hq, N, bwd_dq_rows(d), bwd_dq_dims(d)))
     return ATTN_ERR_CUDA;
-  BwdArgs a{};
+  BwdScoreArgs a{};
   a.lse = lse;
   a.dvec = dvec;
   a.dq_acc = dq_acc;
