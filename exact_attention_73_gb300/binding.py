@@ -147,15 +147,20 @@ def _dims(t, name, n):
     return tuple(t.shape)
 
 
+def _attn_dims(q, k):
+    """B, Hq, Hkv, N, d of q [B,Hq,N,d] and k [B,Hkv,N,d]."""
+    B, Hq, N, d = _dims(q, "q", 4)
+    return B, Hq, _dims(k, "k", 4)[1], N, d
+
+
 def _nb(n):
     return (n + 127) // 128
 
 
-def _bwd_ptrs(q, k, v, o, lse, dout, dq, dk, dv, dev=None):
+def _bwd_ptrs(q, k, v, o, lse, dout, dq, dk, dv, dev=None, dims=None):
     """Pointers of a dense backward call: q [B,Hq,N,d], k/v [B,Hkv,N,d], o, dout,
     dq like q, dk/dv like k (all of q's type), lse [B,Hq,N] float32."""
-    B, Hq, N, d = _dims(q, "q", 4)
-    Hkv = _dims(k, "k", 4)[1]
+    B, Hq, Hkv, N, d = dims or _attn_dims(q, k)
     dt = q.dtype
     kv = (B, Hkv, N, d)
     nq, nk = q.numel(), k.numel()
@@ -169,10 +174,11 @@ def _bwd_ptrs(q, k, v, o, lse, dout, dq, dk, dv, dev=None):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
+    """Handle of `stream`, or of the current one (of device dev, where the caller has asked for it already)."""
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if dev is None else dev)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
@@ -191,11 +197,10 @@ def _dtype(t):
     return _DT[t.dtype]
 
 
-def _fwd_ptrs(q, k, v, o, lse, dev=None):
+def _fwd_ptrs(q, k, v, o, lse, dev=None, dims=None):
     """Pointers of a dense forward call: q [B,Hq,N,d], k/v [B,Hkv,N,d] of q's
     type, o like q, lse [B,Hq,N] float32."""
-    B, Hq, N, d = _dims(q, "q", 4)
-    Hkv = _dims(k, "k", 4)[1]
+    B, Hq, Hkv, N, d = dims or _attn_dims(q, k)
     kv = (B, Hkv, N, d)
     dt = q.dtype
     return [_ptr(q, "q", None, None, None, dev), _ptr(k, "k", None, dt, kv, dev), _ptr(v, "v", None, dt, kv, dev),
@@ -347,15 +352,17 @@ def attn_decode_fp8(q8, sq, k8, v8, sk, sv, o, lse, workspace, num_splits, seqle
                                   B, Hq, Hkv, Nmax, d, scale, int(num_splits), _stream(stream)), "attn_decode_fp8")
 
 
-def _strided(t, name, dev, dtype=None, shape=None):
-    """Pointer and strides of a [B, H, N, d] tensor whose rows are dense (any batch, head and row strides)."""
-    b, h, n, d = _dims(t, name, 4)
+def _strided(t, name, dev, dtype, shape):
+    """Pointer and strides of a tensor of `shape` (b, h, n, d) whose rows are dense (any batch, head and row strides)."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a 4-D tensor")
     if t.get_device() != dev:
         raise _not_here(t, name, dev)
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    b, h, n, d = shape
     sb, sh, sn, se = t.stride()
     if d > 1 and se != 1:
         raise ValueError(f"{name} must have adjacent elements in each row (stride 1 in its last dimension)")
@@ -375,13 +382,14 @@ def attn_rope(x, y, rope_cos, rope_sin, positions=None, interleaved=False, inver
     row strides: the first 2 * rope_cos.shape[1] elements of each row are turned, the rest copied.
     Tables float32 [n_pos, rot_dim/2]; positions int32 [B,N] or None (row n at position n; a negative
     one leaves its row of y as it was). inverse turns back: the backward pass of the rotation."""
-    B, H, N, d = _dims(x, "x", 4)
+    shape = B, H, N, d = _dims(x, "x", 4)
     dev = _current_device()
-    px, sx = _strided(x, "x", dev)
-    py, sy = _strided(y, "y", dev, x.dtype, x.shape)
+    px, sx = _strided(x, "x", dev, x.dtype, shape)
+    py, sy = _strided(y, "y", dev, x.dtype, shape)
     pc, ps, rot, n_pos = _rope_dims(rope_cos, rope_sin, dev)
-    _check(load().attn_rope(px, py, pc, ps, _ptr(positions, "positions", None, torch.int32, (B, N), dev), sx, sy, B, H, N, d, rot, n_pos, int(bool(interleaved)), int(bool(inverse)), _dtype(x),
-                            _stream(stream)), "attn_rope")
+    _check(load().attn_rope(px, py, pc, ps, _ptr(positions, "positions", None, torch.int32, (B, N), dev), sx, sy,
+                            B, H, N, d, rot, n_pos, int(bool(interleaved)), int(bool(inverse)), _dtype(x),
+                            _stream(stream, dev)), "attn_rope")
 
 
 def attn_rope_tables(rope_cos, rope_sin, inv_freq, first_position=0, amplitude=1.0, stream=None):
@@ -390,7 +398,7 @@ def attn_rope_tables(rope_cos, rope_sin, inv_freq, first_position=0, amplitude=1
     dev = _current_device()
     pc, ps, rot, n_pos = _rope_dims(rope_cos, rope_sin, dev)
     _check(load().attn_rope_tables(pc, ps, _ptr(inv_freq, "inv_freq", rot // 2, torch.float64, None, dev),
-                                   int(first_position), n_pos, rot, float(amplitude), _stream(stream)), "attn_rope_tables")
+                                   int(first_position), n_pos, rot, float(amplitude), _stream(stream, dev)), "attn_rope_tables")
 
 
 def attn_mask_rows(row_ranges, doc_ids=None, prefix_lens=None, causal=True, stream=None):
@@ -401,7 +409,7 @@ def attn_mask_rows(row_ranges, doc_ids=None, prefix_lens=None, causal=True, stre
     _check(load().attn_mask_rows(_ptr(doc_ids, "doc_ids", None, i32, (B, N), dev),
                                  _ptr(prefix_lens, "prefix_lens", B, i32, None, dev),
                                  _ptr(row_ranges, "row_ranges", None, i32, (B, N, 2), dev), B, N,
-                                 int(bool(causal)), _stream(stream)), "attn_mask_rows")
+                                 int(bool(causal)), _stream(stream, dev)), "attn_mask_rows")
 
 
 def attn_score_workspace_size(B, N):
@@ -412,17 +420,17 @@ def attn_fwd_score(q, k, v, o, lse, workspace=None, row_ranges=None, slopes=None
                    scale=None, stream=None):
     """Dense forward with scores cap * tanh(s / cap) - slopes[h] |i - j|, key window and row ranges
     int32 [B,N,2] (these need a workspace of attn_score_workspace_size bytes); slopes fp32 [Hq]."""
-    B, Hq, N, d = _dims(q, "q", 4)
-    Hkv = _dims(k, "k", 4)[1]
+    dims = B, Hq, Hkv, N, d = _attn_dims(q, k)
     dev = _current_device()
     scale = 1.0 / math.sqrt(d) if scale is None else scale
-    left, right = (int(w) for w in window)
-    _check(load().attn_fwd_score(*_fwd_ptrs(q, k, v, o, lse, dev),
+    left, right = window
+    _check(load().attn_fwd_score(*_fwd_ptrs(q, k, v, o, lse, dev, dims),
                                  _ptr(row_ranges, "row_ranges", None, torch.int32, (B, N, 2), dev),
                                  _ptr(slopes, "slopes", Hq, torch.float32, None, dev),
                                  _ptr(workspace, "workspace", None, None, None, dev),
                                  0 if workspace is None else workspace.numel() * workspace.element_size(), B, Hq, Hkv,
-                                 N, d, scale, float(score_cap), left, right, _dtype(q), _stream(stream)),
+                                 N, d, scale, float(score_cap), int(left), int(right), _dtype(q),
+                                 _stream(stream, dev)),
            "attn_fwd_score")
 
 
@@ -433,17 +441,17 @@ def attn_bwd_score_workspace_size(B, Hq, Hkv, N, d):
 def attn_bwd_score(q, k, v, o, lse, dout, dq, dk, dv, workspace, row_ranges=None, slopes=None, score_cap=0.0,
                    window=(-1, -1), scale=None, stream=None):
     """Backward of attn_fwd_score; workspace of attn_bwd_score_workspace_size bytes."""
-    B, Hq, N, d = _dims(q, "q", 4)
-    Hkv = _dims(k, "k", 4)[1]
+    dims = B, Hq, Hkv, N, d = _attn_dims(q, k)
     dev = _current_device()
     scale = 1.0 / math.sqrt(d) if scale is None else scale
-    left, right = (int(w) for w in window)
-    _check(load().attn_bwd_score(*_bwd_ptrs(q, k, v, o, lse, dout, dq, dk, dv, dev),
+    left, right = window
+    _check(load().attn_bwd_score(*_bwd_ptrs(q, k, v, o, lse, dout, dq, dk, dv, dev, dims),
                                  _ptr(row_ranges, "row_ranges", None, torch.int32, (B, N, 2), dev),
                                  _ptr(slopes, "slopes", Hq, torch.float32, None, dev),
                                  _ptr(workspace, "workspace", None, None, None, dev),
                                  workspace.numel() * workspace.element_size(), B, Hq, Hkv, N, d, scale,
-                                 float(score_cap), left, right, _dtype(q), _stream(stream)), "attn_bwd_score")
+                                 float(score_cap), int(left), int(right), _dtype(q),
+                                 _stream(stream, dev)), "attn_bwd_score")
 
 
 def _cache_ptrs(k8, v8, sk, sv, block_table, B, Hkv, d, dev):
@@ -471,10 +479,10 @@ def attn_cache_append_fp8(k, v, k8, v8, sk, sv, seqlens, new_lens=None, block_ta
     seqlens[b] rows: dense k8/v8 [B,Hkv,Nmax,d], sk/sv [B,Hkv,ceil(Nmax/128)], or pages
     [P,Hkv,128,d], [P,Hkv] with block_table int32 [B,blocks]. new_lens int32 [B]: rows of k and v that count
     (None: all). Tables given: the keys are rotated first, row r of a sequence at position r."""
-    B, Hkv, n, d = _dims(k, "k", 4)
+    shape = B, Hkv, n, d = _dims(k, "k", 4)
     dev, i32 = _current_device(), torch.int32
-    pk, stk = _strided(k, "k", dev)
-    pv, stv = _strided(v, "v", dev, k.dtype, k.shape)
+    pk, stk = _strided(k, "k", dev, k.dtype, shape)
+    pv, stv = _strided(v, "v", dev, k.dtype, shape)
     (p8k, p8v, psk, psv, pt), rows, pages = _cache_ptrs(k8, v8, sk, sv, block_table, B, Hkv, d, dev)
     if (rope_cos is None) != (rope_sin is None):
         raise ValueError("rope_cos and rope_sin go together")
@@ -482,7 +490,7 @@ def attn_cache_append_fp8(k, v, k8, v8, sk, sv, seqlens, new_lens=None, block_ta
     _check(load().attn_cache_append_fp8(pk, pv, stk, stv, p8k, p8v, psk, psv,
                                         _ptr(seqlens, "seqlens", B, i32, None, dev),
                                         _ptr(new_lens, "new_lens", B, i32, None, dev), pt, pc, ps, B, Hkv, n, rows,
-                                        pages, d, rot, n_pos, int(bool(interleaved)), _dtype(k), _stream(stream)),
+                                        pages, d, rot, n_pos, int(bool(interleaved)), _dtype(k), _stream(stream, dev)),
            "attn_cache_append_fp8")
 
 
@@ -513,7 +521,7 @@ def attn_decode_cache_fp8(q, k8, v8, sk, sv, seqlens, o, lse, workspace, num_spl
                                         _ptr(workspace, "workspace", None, None, None, dev),
                                         workspace.numel() * workspace.element_size(), B, Hq, Hkv, rows, pages, d,
                                         scale, float(score_cap), int(window_left), int(num_splits), _dtype(q),
-                                        _stream(stream)), "attn_decode_cache_fp8")
+                                        _stream(stream, dev)), "attn_decode_cache_fp8")
 
 
 def attn_bwd_workspace_size(B, Hq, Hkv, N, d):
