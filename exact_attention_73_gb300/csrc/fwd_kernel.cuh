@@ -526,16 +526,19 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[t], j & 1, a.status));
         tc_fence_after();
         const bool edge = warp_any(vis.x > kb || vis.y < kb + 64);
-        ScoreTile st = score_bound<kCap, kBias, 2>(tS, a.sc, edge, slope2, kb - qrow);
+        const bool none = vis.x >= kb + 64 || vis.y <= kb;
+        const bool blind = edge && !warp_any(!none);   // none of the warp's rows sees any: zero weights
+        ScoreTile st{};
+        if (!blind) st = score_bound<kCap, kBias, 2>(tS, a.sc, edge, slope2, kb - qrow);
         // no visible score passes the running max by kTau, in either half of
         // the warp's rows: it stays. (A wait that ran out ends both warps in
         // the other branch.)
-        const bool none = vis.x >= kb + 64 || vis.y <= kb;
         if (named_bar_and(pair, 64, ok && (none || st.top <= m + R::kTau))) {
-          if (!st.straight) score_finish<kCap, kBias, 2>(tS, a.sc, st.tier, edge, slope2, kb - qrow, vis.x - kb, vis.y - kb);
+          if (!blind && !st.straight)
+            score_finish<kCap, kBias, 2>(tS, a.sc, st.tier, edge, slope2, kb - qrow, vis.x - kb, vis.y - kb);
         } else {
           float mx = -INFINITY;
-          if (ok) {
+          if (ok && !blind) {
             if (kBias || !st.straight) {   // with a bias the largest raw score need not be the largest
               st.straight = false;
               mx = score_finish<kCap, kBias, 2>(tS, a.sc, st.tier, edge, slope2, kb - qrow, vis.x - kb, vis.y - kb);
@@ -566,7 +569,8 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
           }
         }
         const float bias = m == -INFINITY ? 0.f : -m;
-        l += score_weights<DT == kBF16, kCap, kBias, 2>(tS, a.sc, st.straight ? st.tier : 0, slope2, kb - qrow, bias);
+        if (blind) score_no_weights<2>(tS);
+        else l += score_weights<DT == kBF16, kCap, kBias, 2>(tS, a.sc, st.straight ? st.tier : 0, slope2, kb - qrow, bias);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&p_ready[t]);

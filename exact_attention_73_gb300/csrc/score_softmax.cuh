@@ -164,6 +164,15 @@ __device__ __forceinline__ float score_weights_way(uint32_t tS, const ScoreArgs&
   const float2 s = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
   return s.x + s.y;
 }
+// No visible score: zeros in the weights' places.
+template <int NCH>
+__device__ __forceinline__ void score_no_weights(uint32_t tS) {
+  uint32_t z[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) tmem_st16(tS + (NCH == 4 ? 16 : 32) * c, z);
+}
 template <bool kBF16, bool kCap, bool kBias, int NCH>
 __device__ __forceinline__ float score_weights(uint32_t tS, const ScoreArgs& sc, int way, float slope2, int dist,
                                                float bias) {
