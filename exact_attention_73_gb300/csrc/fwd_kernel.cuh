@@ -665,6 +665,16 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[sb], sphase, a.status));
         if (!ok) break;
         tc_fence_after();
+        if constexpr (kScore != 0) {
+          const int k0 = (kv0 + ((kScore & kScoreBias) ? nkv - 1 - j : j)) * 128;
+          if (!warp_any(vis.x < k0 + 128 && vis.y > k0)) {   // none of the warp's rows sees any: zero weights
+            score_no_weights<4>(tS);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_ready[sb]);
+            continue;
+          }
+        }
         constexpr bool kCap = (kScore & kScoreCap) != 0, kBias = (kScore & kScoreBias) != 0;
         constexpr bool kChanged = kCap || kBias;
         constexpr float kTau = kChanged ? R::kTau : C::kTau;
