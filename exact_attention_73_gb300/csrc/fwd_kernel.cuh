@@ -112,7 +112,7 @@ struct FwdCfg {
 // Two-tile instances with capped or biased scores give each query row two
 // threads, in warpgroups of their own, that take half of the keys each: the
 // longer way from score to weight is latency that one softmax warp per query
-// tile and scheduler cannot hide (four threads per row: 576 against 508 us at
+// tile and scheduler cannot hide (four threads per row: 576 against 505 us at
 // B = 1, Hq = 32, N = 8192, d = 128, causal, cap 50; one-thread rows with d =
 // 256 have twice the products per score to hide it). 640 threads: the load/MMA
 // warpgroup keeps 64 registers, the four softmax warpgroups have 104.
@@ -127,7 +127,7 @@ struct FwdSplit {
   // as their type holds: 16-bit floats round a large one no worse, O and its
   // sum are FP32, and what lies far below the running max only gains. BF16 has
   // the exponents for 40 and more (with a cap the max then hardly ever moves
-  // after a row's first tile), FP16 for 15. Against 8 for both: 590 -> 509 us
+  // after a row's first tile), FP16 for 15. Against 8 for both: 590 -> 515 us
   // at scores of standard deviation 4 and a cap of 50 (B = 1, Hq = 32, N =
   // 8192, d = 128, causal).
   static constexpr float kTau = DT == kBF16 ? 40.f : 15.f;
@@ -248,9 +248,12 @@ __device__ __forceinline__ bool fwd_unit(const FwdArgs& a, int lin, FwdUnit& w) 
 // max starts near the row's own position, where the bias is least.
 //
 // Score instances, B = 1, Hq = 32, Hkv = 8, N = 8192, d = 128, causal, bf16:
-// cap 507 us (1085 TFLOP/s), bias 443, both 576, ranges alone 379, the plain
+// cap 505 us (1090 TFLOP/s), bias 433, both 550, ranges alone 374, the plain
 // kernel 382. The capped softmax is bound by the FMA, MUFU and ALU pipes
-// together, some 2100 cycles of a scheduler per 128 x 128 scores.
+// together, some 2100 cycles of a scheduler per 128 x 128 scores. A warp whose
+// rows see none of its keys (past the diagonal, before a document) writes zero
+// weights at once: 12 documents in 16384 rows at d = 64, bias, 196 -> 174 us
+// (by chunks of 32 keys instead, its bookkeeping spilled: cap 523).
 template <int DT, int D, int QT, bool kPersist, int kScore = 0>
 __global__ void __launch_bounds__(FwdSplit<DT, D, QT, kScore>::NTHREADS, 1)
 fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,

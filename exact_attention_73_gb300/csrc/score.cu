@@ -16,7 +16,7 @@
 // short and bound by latency, so each is a programmatic dependent of the one
 // before it, and so is the kernel behind them: the forward sets itself up
 // meanwhile, and the backward's row sums, which need no facts, run beside them
-// (12 documents in 16384 rows, 16 heads, d = 64: 209 -> 196 us).
+// (12 documents in 16384 rows, 16 heads, d = 64: 13 us less).
 #include <climits>
 #include <cmath>
 #include <cstdint>
