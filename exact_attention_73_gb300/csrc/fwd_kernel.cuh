@@ -120,6 +120,7 @@ template <int DT, int D, int QT, int kScore>
 struct FwdSplit {
   using C = FwdCfg<DT, D, QT>;
   static constexpr bool kRows = QT == 2 && (kScore & (kScoreCap | kScoreBias)) != 0;
+  static_assert(!(kScore & kScoreFixed) || (kRows && DT == kBF16 && !(kScore & kScoreBias)), "weights without a max");
   static constexpr int NTHREADS = kRows ? 640 : C::NTHREADS;
   static constexpr uint32_t kRegsCtl = kRows ? 64 : C::kRegsCtl, kRegsSoft = kRows ? 104 : C::kRegsSoft;
   static_assert(!kRows || 128 * kRegsCtl + 512 * kRegsSoft <= 640 * 96, "register split");
@@ -530,6 +531,16 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         tc_fence_after();
         const bool edge = warp_any(vis.x > kb || vis.y < kb + 64);
         const bool none = vis.x >= kb + 64 || vis.y <= kb;
+        if constexpr ((kScore & kScoreFixed) != 0) {
+          if (!ok) break;
+          m = 0.f;
+          if (edge && !warp_any(!none)) score_no_weights<2>(tS);
+          else l += score_fixed_weights<DT == kBF16, 2>(tS, a.sc, edge, vis.x - kb, vis.y - kb);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&p_ready[t]);
+          continue;
+        }
         const bool blind = edge && !warp_any(!none);   // none of the warp's rows sees any: zero weights
         ScoreTile st{};
         if (!blind) st = score_bound<kCap, kBias, 2>(tS, a.sc, edge, slope2, kb - qrow);

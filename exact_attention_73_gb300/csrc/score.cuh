@@ -23,7 +23,14 @@ namespace attn {
 // 0 is the plain kernel. Each has its own instances because a branch in the
 // softmax loops costs registers they do not have (one instance for all of
 // them ran the uncapped backward 27 % slower at d = 128).
-enum : int { kScoreCap = 1, kScoreBias = 2, kScoreRanges = 4 };
+enum : int { kScoreCap = 1, kScoreBias = 2, kScoreRanges = 4, kScoreFixed = 8 };
+
+// kScoreFixed (forward, with a cap, without a bias, BF16 weights): capped
+// scores lie within +-cap log2(e), so with a small cap exp2(x) itself is the
+// weight and there is no running max. Relative rounding does not change; the
+// sums stay below 2^(80 + 24) |V| (N <= 2^24), and a row whose scores are all
+// at -cap still has its weights 46 bits above the smallest normal float.
+constexpr float kFixedMax = 80.f;   // largest cap, log2 units
 
 struct ScoreArgs {
   const int2* ranges;       // [B, N] visible keys [x, y) of each row, or null

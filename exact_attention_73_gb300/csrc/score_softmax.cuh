@@ -182,4 +182,56 @@ __device__ __forceinline__ float score_weights(uint32_t tS, const ScoreArgs& sc,
   return score_weights_way<kBF16, kCap, kBias, NCH, kCap ? 3 : 1>(tS, sc, slope2, dist, bias);
 }
 
+// kScoreFixed: raw scores to weights in one pass, exp2 of the capped scores;
+// columns lo <= c < hi are visible (edge: some are not). Returns their sum.
+template <bool kBF16, int NCH>
+__device__ __forceinline__ float score_fixed_weights(uint32_t tS, const ScoreArgs& sc, bool edge, int lo, int hi) {
+  float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+  for (int c = 0; c < NCH; ++c) {
+    uint32_t r[32], pk[16];
+    tmem_ld32(tS + 32 * c, r);
+    tmem_wait_ld();
+    reg_fence(r);
+    const float big = rowmax_abs(r);
+    if (!edge && !warp_any(!(big <= sc.s_small))) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float2 s = make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+        float2 x = fmul2(s, cap_small_factor(s, sc));
+        x = make_float2(ex2(x.x), ex2(x.y));
+        acc[e & 3] = fadd2(acc[e & 3], x);
+        pk[e] = kBF16 ? pack_bf16x2(x.x, x.y) : pack_f16x2(x.x, x.y);
+      }
+    } else {
+      if (!warp_any(!(big * fabsf(sc.w_of_s) <= 1.f))) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 y = cap_pair(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), sc.w_of_s, sc.cap_log2);
+          r[e] = __float_as_uint(y.x);
+          r[e + 1] = __float_as_uint(y.y);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(cap_any(__uint_as_float(r[e]), sc.w_of_s, sc.cap_log2));
+      }
+      if (edge) {
+        const int l = lo - 32 * c, h = hi - 32 * c;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (e >= h || e < l) r[e] = __float_as_uint(-INFINITY);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float2 x = make_float2(ex2(__uint_as_float(r[2 * e])), ex2(__uint_as_float(r[2 * e + 1])));
+        acc[e & 3] = fadd2(acc[e & 3], x);
+        pk[e] = kBF16 ? pack_bf16x2(x.x, x.y) : pack_f16x2(x.x, x.y);
+      }
+    }
+    tmem_st16(tS + (NCH == 4 ? 16 : 32) * c, pk);
+  }
+  const float2 s = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+  return s.x + s.y;
+}
+
 }  // namespace attn
