@@ -249,9 +249,11 @@ __device__ __forceinline__ bool fwd_unit(const FwdArgs& a, int lin, FwdUnit& w) 
 // max starts near the row's own position, where the bias is least.
 //
 // Score instances, B = 1, Hq = 32, Hkv = 8, N = 8192, d = 128, causal, bf16:
-// cap 505 us (1090 TFLOP/s), bias 433, both 550, ranges alone 374, the plain
-// kernel 382. The capped softmax is bound by the FMA, MUFU and ALU pipes
-// together, some 2100 cycles of a scheduler per 128 x 128 scores. A warp whose
+// cap 437 us (1258 TFLOP/s; 505 with a running max), bias 433, both 550, ranges
+// alone 374, the plain kernel 382. Bound by latency: of a step's 4830 cycles
+// (with the max) a scheduler issues in 43 %, and the tensor pipe is busy for
+// 42 %; the softmax of a tile and its two products follow one another, and
+// tensor memory has no room for a second score buffer at d = 128. A warp whose
 // rows see none of its keys (past the diagonal, before a document) writes zero
 // weights at once: 12 documents in 16384 rows at d = 64, bias, 196 -> 174 us
 // (by chunks of 32 keys instead, its bookkeeping spilled: cap 523).

@@ -183,7 +183,8 @@ __device__ __forceinline__ float score_weights(uint32_t tS, const ScoreArgs& sc,
 }
 
 // kScoreFixed: raw scores to weights in one pass, exp2 of the capped scores;
-// columns lo <= c < hi are visible (edge: some are not). Returns their sum.
+// columns lo <= c < hi are visible (edge: some are not). Returns their sum. (Both
+// chunks read at once and unrolled spill: 443 against 437 us.)
 template <bool kBF16, int NCH>
 __device__ __forceinline__ float score_fixed_weights(uint32_t tS, const ScoreArgs& sc, bool edge, int lo, int hi) {
   float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};

@@ -156,6 +156,36 @@ def test_masks_of_more_rows_than_one_block_takes(cap, slopes):
         assert not x[:, :, N - 130:].any()
 
 
+@pytest.mark.parametrize("cap", [5.0, 55.0, 56.0, 300.0])
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (128, "fp16"), (256, "bf16")])
+@pytest.mark.parametrize("ranges", [False, True])
+def test_scores_at_either_end_of_the_cap(cap, d, dtype, ranges):
+    """Every score of a head at -cap, at +cap, or the rows' own half at one and the rest at the other, whatever the
+    cap: weights without a running max (small caps) or with one give the same attention."""
+    B, H, N = 1, 3, 300
+    r = np.random.default_rng(54)
+    q = np.abs(r.standard_normal((B, H, N, d))) + 0.5
+    k = np.abs(r.standard_normal((B, H, N, d))) + 0.5
+    q *= 8 * cap / d ** 0.5               # q.k / sqrt(d) is at least 2 cap: tanh within 4 % of one, mostly at one
+    k[:, 0] *= -1
+    k[:, 2, ::2] *= -1
+    q, k, v = (torch.from_numpy(x).to({"bf16": torch.bfloat16, "fp16": torch.float16}[dtype])
+               for x in (q, k, r.standard_normal((B, H, N, d))))
+    m = masks(55, B, N, 1)[0] if ranges else None
+    o, lse = torch.full_like(q, float("nan")).cuda(), torch.full((B, H, N), float("nan"), device="cuda")
+    L.attn_fwd_score(q.cuda(), k.cuda(), v.cuda(), o, lse, row_ranges=m, score_cap=cap, window=(-1, 0),
+                     workspace=torch.empty(L.attn_score_workspace_size(B, N), dtype=U8, device="cuda"))
+    assert L.attn_get_device_status() == 0
+    rm = None if m is None else m.cpu().numpy()
+    ro, rl = S.forward(q, k, v, d ** -0.5, rm, (-1, 0), cap)
+    mag, _ = S.forward(q, k, v.abs(), d ** -0.5, rm, (-1, 0), cap)
+    # the capped score is off by 6e-7 of itself (cap) and 2^-22 of it (float32), both in the exponent
+    half, dx = torch.finfo(q.dtype).eps / 2, cap * (6e-7 + 2.0 ** -22)
+    tol = (half + 2 * dx + 2.0 ** -20) * (1 + half) * mag + half * np.abs(ro) + 2.0 ** -25
+    assert (np.abs(o.double().cpu().numpy() - ro) <= tol).all()
+    assert (np.abs(lse.double().cpu().numpy() - rl) <= dx + 2.0 ** -20 * (1 + np.abs(rl))).all()
+
+
 @pytest.mark.parametrize("B,N", [(2, 500), (20, 1000)])
 def test_one_workspace_used_again_at_once(B, N):
     """Calls behind one another with other masks and one workspace: each sees its own tile facts."""
