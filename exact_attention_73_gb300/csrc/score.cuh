@@ -27,9 +27,10 @@ enum : int { kScoreCap = 1, kScoreBias = 2, kScoreRanges = 4, kScoreFixed = 8 };
 
 // kScoreFixed (forward, with a cap, without a bias, BF16 weights): capped
 // scores lie within +-cap log2(e), so with a small cap exp2(x) itself is the
-// weight and there is no running max. Relative rounding does not change; the
-// sums stay below 2^(80 + 24) |V| (N <= 2^24), and a row whose scores are all
-// at -cap still has its weights 46 bits above the smallest normal float.
+// weight and there is no running max. Relative rounding does not change. The
+// sums stay below 2^96 |V|, which leaves V 31 bits, and a row whose scores are
+// all at -cap has its weights 46 bits above the smallest normal float.
+constexpr float kFixedSum = 96.f;   // largest cap in log2 units and log2 of the row length together
 constexpr float kFixedMax = 80.f;   // largest cap, log2 units
 
 struct ScoreArgs {
