@@ -133,7 +133,12 @@ struct FwdSplit {
   // 8192, d = 128, causal).
   static constexpr float kTau = DT == kBF16 ? 40.f : 15.f;
   static constexpr int XCH_B = kRows ? 2 * 2 * 128 * 4 : 0;   // row facts the two threads of a row exchange
-  static constexpr int SMEM_BYTES = C::SMEM_BYTES + XCH_B;
+  // Without a running max the two halves of a score tile have nothing to agree
+  // on, so each (query tile, half of the keys) is a chain of its own: four
+  // chains take turns at the tensor pipe instead of two.
+  static constexpr bool kHalves = (kScore & kScoreFixed) != 0;
+  static constexpr int SMEM_BYTES = C::SMEM_BYTES + XCH_B + (kHalves ? 64 : 0);   // and their barriers
+  static constexpr uint32_t IDESC_H = instr_desc(128, 64, C::FMT, C::FMT, 0, 0);
 };
 
 __device__ __forceinline__ int pow2_exponent_of(float x) {   // x an exact power of two
@@ -278,6 +283,9 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
   uint64_t* o_done = o_final + 1;                  // one phase per O += P V (single-tile CTAs)
   uint64_t* q_empty = o_done + 1;                  // the unit's products have read Q
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(q_empty + 1);
+  // kHalves: [query tile][half] in the places of s_full and p_ready
+  uint64_t* s_half = reinterpret_cast<uint64_t*>(smem + C::SMEM_BYTES - 1024 + R::XCH_B);
+  uint64_t* p_half = s_half + 4;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -305,6 +313,12 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     for (int t = 0; t < C::NSB; ++t) {
       mbar_init(&s_full[t], 1);
       mbar_init(&p_ready[t], R::kRows ? 256 : 128);
+    }
+    if constexpr (R::kHalves) {
+      for (int h = 0; h < 4; ++h) {
+        mbar_init(&s_half[h], 1);
+        mbar_init(&p_half[h], 128);
+      }
     }
     mbar_init(o_final, 1);
     mbar_init(o_done, 1);
@@ -410,6 +424,26 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                           (j > 0 || kk > 0) ? 1u : 0u);
         }
       };
+      // kHalves: S_t and P V of half p of the keys, columns t * 128 + p * 64 ..
+      auto issue_s_half = [&](int t, int p, int slot) {
+#pragma unroll
+        for (int kk = 0; kk < D / C::KSTEP_E; ++kk) {
+          const uint32_t off = (kk * C::KSTEP_B / C::BOX_B) * C::BOXT_B + (kk * C::KSTEP_B) % C::BOX_B;
+          const uint64_t ad = smem_desc(q_addr + t * C::TILE_B + off, 16, C::SBO, C::SWZ);
+          const uint64_t bd = smem_desc(kv_addr + slot * C::TILE_B + off + p * 64 * C::BOX_B, 16, C::SBO, C::SWZ);
+          mma_ss<C::kFp8>(tbase + t * 128 + p * 64, ad, bd, R::IDESC_H, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&s_half[2 * t + p]);
+      };
+      auto issue_pv_half = [&](int t, int p, int slot, int j) {
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+          const uint64_t bd = smem_desc(kv_addr + slot * C::TILE_B + (4 * p + k4) * C::KSTEP_E * C::BOX_B, C::BOXT_B,
+                                        C::SBO, C::SWZ);
+          mma_ts<C::kFp8>(tbase + C::O_COL + t * D, tbase + t * 128 + p * 64 + (k4 >> 1) * 32 + (k4 & 1) * 8, bd,
+                          C::IDESC_O, (j > 0 || p > 0 || k4 > 0) ? 1u : 0u);
+        }
+      };
       // K/V tile `it` of this unit
       auto kv_wait = [&](int it) {
         return mbar_wait(&kv_full[(kvb + it) % C::NSLOT], ((kvb + it) / C::NSLOT) & 1, a.status);
@@ -455,6 +489,32 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
               issue_s(0, sb, kv_slot(itk));
               mma_commit(&kv_empty[kv_slot(itk)]);
             }
+          }
+        } else if constexpr (R::kHalves) {
+          // as below, by halves: PV_t,p(j), S_t,p(j+1) for p, for t
+          if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 4; ++h) issue_s_half(h & 1, h >> 1, kv_slot(0));
+            mma_commit(&kv_empty[kv_slot(0)]);
+          }
+          for (int j = 0; j < nkv && ok; ++j) {
+            const int itv = 2 * j + 1, sv_ = kv_slot(itv);
+            const int itk = 2 * j + 2, sk_ = kv_slot(itk);
+            const bool next = j + 1 < nkv;
+            if (!(ok = kv_wait(itv))) break;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const int t = h & 1, p = h >> 1;
+              ok = ok && mbar_wait(&p_half[2 * t + p], j & 1, a.status);
+              if (!ok) break;
+              if (next && h == 0 && !(ok = kv_wait(itk))) break;   // K(j+1)
+              tc_fence_after();
+              issue_pv_half(t, p, sv_, j);
+              if (next) issue_s_half(t, p, sk_);
+            }
+            mma_commit(&kv_empty[sv_]);
+            if (next && ok) mma_commit(&kv_empty[sk_]);
           }
         } else {
           // Issue order: S_t(0) for every tile, then per KV step j:
@@ -529,7 +589,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       bool ok = unit;
       for (int j = 0; j < w.nkv; ++j) {
         const int kb = (w.kv0 + (kBias ? w.nkv - 1 - j : j)) * 128 + part * 64;   // first key of this half
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[t], j & 1, a.status));
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(R::kHalves ? &s_half[2 * t + part] : &s_full[t], j & 1, a.status));
         tc_fence_after();
         const bool edge = warp_any(vis.x > kb || vis.y < kb + 64);
         const bool none = vis.x >= kb + 64 || vis.y <= kb;
@@ -540,7 +600,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
           else l += score_fixed_weights<DT == kBF16, 2>(tS, a.sc, edge, vis.x - kb, vis.y - kb);
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(&p_ready[t]);
+          mbar_arrive(&p_half[2 * t + part]);
           continue;
         }
         const bool blind = edge && !warp_any(!none);   // none of the warp's rows sees any: zero weights
