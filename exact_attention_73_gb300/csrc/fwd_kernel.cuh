@@ -135,7 +135,10 @@ struct FwdSplit {
   static constexpr int XCH_B = kRows ? 2 * 2 * 128 * 4 : 0;   // row facts the two threads of a row exchange
   // Without a running max the two halves of a score tile have nothing to agree
   // on, so each (query tile, half of the keys) is a chain of its own: four
-  // chains take turns at the tensor pipe instead of two.
+  // chains take turns at the tensor pipe instead of two (cap 50 as below 437 ->
+  // 431 us, the exact tanh 722 -> 658, five documents 184 -> 175; with the
+  // score products whole and only P V by halves 441). Their N = 64 products
+  // read Q twice as often, and that is what bounds them.
   static constexpr bool kHalves = (kScore & kScoreFixed) != 0;
   static constexpr int SMEM_BYTES = C::SMEM_BYTES + XCH_B + (kHalves ? 64 : 0);   // and their barriers
   static constexpr uint32_t IDESC_H = instr_desc(128, 64, C::FMT, C::FMT, 0, 0);
@@ -254,12 +257,12 @@ __device__ __forceinline__ bool fwd_unit(const FwdArgs& a, int lin, FwdUnit& w) 
 // max starts near the row's own position, where the bias is least.
 //
 // Score instances, B = 1, Hq = 32, Hkv = 8, N = 8192, d = 128, causal, bf16:
-// cap 437 us (1258 TFLOP/s; 505 with a running max), bias 433, both 550, ranges
-// alone 374, the plain kernel 382. Bound by latency: of a step's 4830 cycles
-// (with the max) a scheduler issues in 43 %, and the tensor pipe is busy for
-// 42 %; the softmax of a tile and its two products follow one another, and
-// tensor memory has no room for a second score buffer at d = 128. A warp whose
-// rows see none of its keys (past the diagonal, before a document) writes zero
+// cap 431 us (1276 TFLOP/s; 505 with a running max), bias 433, both 550, ranges
+// alone 374, the plain kernel 382. Those with a running max are bound by
+// latency: of a step's 4830 cycles a scheduler issues in 43 %, and the tensor
+// pipe is busy for 42 %; the softmax of a tile and its two products follow one
+// another, and tensor memory has no room for a second score buffer at d = 128.
+// A warp whose rows see none of its keys (past the diagonal, before a document) writes zero
 // weights at once: 12 documents in 16384 rows at d = 64, bias, 196 -> 174 us
 // (by chunks of 32 keys instead, its bookkeeping spilled: cap 523).
 template <int DT, int D, int QT, bool kPersist, int kScore = 0>
