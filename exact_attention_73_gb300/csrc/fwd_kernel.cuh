@@ -132,14 +132,19 @@ struct FwdSplit {
   // at scores of standard deviation 4 and a cap of 50 (B = 1, Hq = 32, N =
   // 8192, d = 128, causal).
   static constexpr float kTau = DT == kBF16 ? 40.f : 15.f;
-  static constexpr int XCH_B = kRows ? 2 * 2 * 128 * 4 : 0;   // row facts the two threads of a row exchange
-  // Without a running max the two halves of a score tile have nothing to agree
+  // At d = 64 tensor memory has room for an O of each half of the keys: with a
+  // running max of its own a half needs nothing of the other until the end, and
+  // is a chain of its own too (H = 16, N = 16384, causal, FP16: cap 890 -> 765
+  // us, bias 685 -> 638, both 924 -> 879).
+  static constexpr bool kOwn = kRows && D == 64 && !(kScore & kScoreFixed);
+  static constexpr int XCH_B = kRows ? (kOwn ? 2 : 1) * 2 * 2 * 128 * 4 : 0;   // row facts the two threads of a row exchange
+  // kHalves. Without a running max the two halves of a score tile have nothing to agree
   // on, so each (query tile, half of the keys) is a chain of its own: four
   // chains take turns at the tensor pipe instead of two (cap 50 as below 437 ->
   // 431 us, the exact tanh 722 -> 658, five documents 184 -> 175; with the
   // score products whole and only P V by halves 441). Their N = 64 products
   // read Q twice as often, and that is what bounds them.
-  static constexpr bool kHalves = (kScore & kScoreFixed) != 0;
+  static constexpr bool kHalves = (kScore & kScoreFixed) != 0 || kOwn;
   static constexpr int SMEM_BYTES = C::SMEM_BYTES + XCH_B + (kHalves ? 64 : 0);   // and their barriers
   static constexpr uint32_t IDESC_H = instr_desc(128, 64, C::FMT, C::FMT, 0, 0);
 };
@@ -262,9 +267,10 @@ __device__ __forceinline__ bool fwd_unit(const FwdArgs& a, int lin, FwdUnit& w) 
 // latency: of a step's 4830 cycles a scheduler issues in 43 %, and the tensor
 // pipe is busy for 42 %; the softmax of a tile and its two products follow one
 // another, and tensor memory has no room for a second score buffer at d = 128.
-// A warp whose rows see none of its keys (past the diagonal, before a document) writes zero
-// weights at once: 12 documents in 16384 rows at d = 64, bias, 196 -> 174 us
-// (by chunks of 32 keys instead, its bookkeeping spilled: cap 523).
+// A warp whose rows see none of its keys (past the diagonal, before a
+// document) writes zero weights at once: 12 documents in 16384 rows at d = 64,
+// bias, 196 -> 174 us (by chunks of 32 keys instead, its bookkeeping spilled:
+// cap 523).
 template <int DT, int D, int QT, bool kPersist, int kScore = 0>
 __global__ void __launch_bounds__(FwdSplit<DT, D, QT, kScore>::NTHREADS, 1)
 fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -443,8 +449,9 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         for (int k4 = 0; k4 < 4; ++k4) {
           const uint64_t bd = smem_desc(kv_addr + slot * C::TILE_B + (4 * p + k4) * C::KSTEP_E * C::BOX_B, C::BOXT_B,
                                         C::SBO, C::SWZ);
-          mma_ts<C::kFp8>(tbase + C::O_COL + t * D, tbase + t * 128 + p * 64 + (k4 >> 1) * 32 + (k4 & 1) * 8, bd,
-                          C::IDESC_O, (j > 0 || p > 0 || k4 > 0) ? 1u : 0u);
+          mma_ts<C::kFp8>(tbase + C::O_COL + (R::kOwn ? 2 * t + p : t) * D,
+                          tbase + t * 128 + p * 64 + (k4 >> 1) * 32 + (k4 & 1) * 8, bd, C::IDESC_O,
+                          (j > 0 || k4 > 0 || (p > 0 && !R::kOwn)) ? 1u : 0u);
         }
       };
       // K/V tile `it` of this unit
@@ -575,7 +582,8 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       const int quarter = warp & 3;
       const int row = quarter * 32 + lane;
       const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-      const uint32_t tO = tbase + lane_off + C::O_COL + t * D + part * (D / 2);
+      // this thread's part of O: half of the dims, or (kOwn) all of its half of the keys
+      const uint32_t tO = tbase + lane_off + C::O_COL + (R::kOwn ? (2 * t + part) * D : t * D + part * (D / 2));
       const uint32_t tS = tbase + lane_off + t * 128 + part * 64;
       const uint32_t pair = 1 + t * 4 + quarter;      // named barrier of the two warps of these 32 rows
       float* xch = reinterpret_cast<float*>(smem + C::SMEM_BYTES - 1024) + t * 256;   // [part][row]
@@ -612,7 +620,14 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         // no visible score passes the running max by kTau, in either half of
         // the warp's rows: it stays. (A wait that ran out ends both warps in
         // the other branch.)
-        if (named_bar_and(pair, 64, ok && (none || st.top <= m + R::kTau))) {
+        bool keep;
+        if constexpr (R::kOwn) {
+          if (!ok) break;
+          keep = !warp_any(!(none || st.top <= m + R::kTau));
+        } else {
+          keep = named_bar_and(pair, 64, ok && (none || st.top <= m + R::kTau));
+        }
+        if (keep) {
           if (!blind && !st.straight)
             score_finish<kCap, kBias, 2>(tS, a.sc, st.tier, edge, slope2, kb - qrow, vis.x - kb, vis.y - kb);
         } else {
@@ -625,9 +640,11 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
               mx = cap_by(st.tier, score_rowmax<false, 2>(tS), a.sc);
             }
           }
-          xch[part * 128 + row] = mx;
-          if (!(ok = named_bar_and(pair, 64, ok))) break;
-          mx = fmaxf(mx, xch[(part ^ 1) * 128 + row]);
+          if constexpr (!R::kOwn) {
+            xch[part * 128 + row] = mx;
+            if (!(ok = named_bar_and(pair, 64, ok))) break;
+            mx = fmaxf(mx, xch[(part ^ 1) * 128 + row]);
+          }
           float corr = 1.f;
           if (mx > m + R::kTau) {
             corr = ex2(m - mx);   // m = -inf gives 0
@@ -636,7 +653,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
           l *= corr;
           if (j > 0 && warp_any(corr != 1.f)) {
 #pragma unroll 1
-            for (int c = 0; c < D / 64; ++c) {
+            for (int c = 0; c < D / (R::kOwn ? 32 : 64); ++c) {
               uint32_t r[32];
               tmem_ld32(tO + 32 * c, r);
               tmem_wait_ld();
@@ -652,28 +669,50 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         else l += score_weights<DT == kBF16, kCap, kBias, 2>(tS, a.sc, st.straight ? st.tier : 0, slope2, kb - qrow, bias);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&p_ready[t]);
+        mbar_arrive(R::kHalves ? &p_half[2 * t + part] : &p_ready[t]);
       }
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_final, 0, a.status));
       tc_fence_after();
-      if (ok) xch[part * 128 + row] = l;   // its last reads were before the step's barrier
+      if (ok) {   // the last reads of xch were before the step's barrier
+        xch[part * 128 + row] = l;
+        if constexpr (R::kOwn) xch[512 + part * 128 + row] = m;
+      }
       if (named_bar_and(pair, 64, ok)) {
-        l += xch[(part ^ 1) * 128 + row];
+        float mine = 1.f, other = 1.f;   // kOwn: weights of the two halves' O
+        if constexpr (R::kOwn) {
+          const float m2 = xch[512 + (part ^ 1) * 128 + row], top = fmaxf(m, m2);
+          mine = m == -INFINITY ? 0.f : ex2(m - top);
+          other = m2 == -INFINITY ? 0.f : ex2(m2 - top);
+          m = top;
+        }
+        l = l * mine + xch[(part ^ 1) * 128 + row] * other;
         const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees nothing: O = 0, LSE = -inf
+        mine *= inv;
+        other *= inv;
         const bool valid = qrow < L;
         const long long row_off = static_cast<long long>(w.b) * a.o_sb + static_cast<long long>(w.h) * a.o_sh +
                                   static_cast<long long>(qrow) * a.o_sn + part * (D / 2);
 #pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
-          uint32_t r[32];
-          tmem_ld32(tO + 32 * c, r);
+          uint32_t r[32], r2[R::kOwn ? 32 : 1];
+          if constexpr (R::kOwn) {   // this half of the dims of both halves of the keys
+            tmem_ld32(tO + part * 32 + 32 * c, r);
+            tmem_ld32(tbase + lane_off + C::O_COL + (2 * t + (part ^ 1)) * D + part * 32 + 32 * c, r2);
+          } else {
+            tmem_ld32(tO + 32 * c, r);
+          }
           tmem_wait_ld();
           reg_fence(r);
+          if constexpr (R::kOwn) reg_fence(r2);
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float x0 = __uint_as_float(r[2 * e]) * inv;
-            const float x1 = __uint_as_float(r[2 * e + 1]) * inv;
+            float x0 = __uint_as_float(r[2 * e]) * mine;
+            float x1 = __uint_as_float(r[2 * e + 1]) * mine;
+            if constexpr (R::kOwn) {
+              x0 = fmaf(__uint_as_float(r2[2 * e]), other, x0);
+              x1 = fmaf(__uint_as_float(r2[2 * e + 1]), other, x1);
+            }
             pk[e] = (DT == kFP16) ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
           }
           if (valid) {
