@@ -138,12 +138,13 @@ struct FwdSplit {
   // us, bias 685 -> 638, both 924 -> 879).
   static constexpr bool kOwn = kRows && D == 64 && !(kScore & kScoreFixed);
   static constexpr int XCH_B = kRows ? (kOwn ? 2 : 1) * 2 * 2 * 128 * 4 : 0;   // row facts the two threads of a row exchange
-  // kHalves. Without a running max the two halves of a score tile have nothing to agree
-  // on, so each (query tile, half of the keys) is a chain of its own: four
-  // chains take turns at the tensor pipe instead of two (cap 50 as below 437 ->
-  // 431 us, the exact tanh 722 -> 658, five documents 184 -> 175; with the
-  // score products whole and only P V by halves 441). Their N = 64 products
-  // read Q twice as often, and that is what bounds them.
+  // kHalves: without a running max the two halves of a score tile have nothing
+  // to agree on, so each (query tile, half of the keys) is a chain of its own:
+  // four chains take turns at the tensor pipe instead of two (cap 50 as below
+  // 437 -> 431 us, the exact tanh 722 -> 658, five documents 184 -> 175; with
+  // the score products whole and only P V by halves 441; tile 0's halves before
+  // tile 1's 441). What they cost is issue: 48 products a step from one thread
+  // in place of 32 (with the descriptors not constant 508 us).
   static constexpr bool kHalves = (kScore & kScoreFixed) != 0 || kOwn;
   static constexpr int SMEM_BYTES = C::SMEM_BYTES + XCH_B + (kHalves ? 64 : 0);   // and their barriers
   static constexpr uint32_t IDESC_H = instr_desc(128, 64, C::FMT, C::FMT, 0, 0);
