@@ -883,7 +883,7 @@ extern "C" attn_status attn_decode_cache_fp8(const void* q, const void* k8, cons
     if (!aligned16(p)) return ATTN_ERR_ALIGN;
   if (B < 1 || B > 65535 || Hq < 1 || Hkv < 1 || Nmax < 1 || Nmax > 0x7fffff00 || window_left < -1) return ATTN_ERR_SHAPE;
   if (block_table && (num_pages < 1 || Nmax % 128)) return ATTN_ERR_SHAPE;
-  if (!(score_cap >= 0.f) || std::isinf(score_cap)) return ATTN_ERR_SHAPE;
+  if (!cap_in_range(scale, score_cap)) return ATTN_ERR_SHAPE;
   if (d != 64 && d != 128 && d != 256) return ATTN_ERR_HEADDIM;
   if (Hq % Hkv) return ATTN_ERR_GQA;
   if (dtype != ATTN_BF16 && dtype != ATTN_FP16) return ATTN_ERR_DTYPE;

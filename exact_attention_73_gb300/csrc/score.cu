@@ -288,7 +288,7 @@ attn_status check_score(const int* row_ranges, const float* slopes, float scale,
   if ((row_ranges && !aligned16(row_ranges)) || (slopes && !aligned16(slopes))) return ATTN_ERR_ALIGN;
   if (left < -1 || right < -1 || N > (1 << 24)) return ATTN_ERR_SHAPE;   // distances are exact in float32
   // the running max follows the largest q.k, and a masked score is -inf times the scale: scale > 0
-  if (!(cap >= 0.f) || std::isinf(cap) || !(scale > 0.f) || std::isinf(scale)) return ATTN_ERR_SHAPE;
+  if (!cap_in_range(scale, cap) || !(scale > 0.f) || std::isinf(scale)) return ATTN_ERR_SHAPE;
   return ATTN_OK;
 }
 

@@ -51,6 +51,16 @@ struct ScoreArgs {
 constexpr float kTanhSmall = 0.5f;
 constexpr float kTanh7[4] = {0.999999456f, -0.333263179f, 0.131902966f, -0.0444022261f};
 
+// Host: a cap that the kernels take: none, or one whose square, and whose
+// ratio to the scale, stay well inside FP32 (beyond them zero times infinity
+// would turn up).
+inline bool cap_in_range(float scale, float cap) {
+  if (cap == 0.f) return true;
+  if (!(cap >= 1e-12f && cap <= 1e30f)) return false;
+  const double r = std::fabs(static_cast<double>(scale)) / cap;
+  return r <= 1e30 && (r == 0.0 || r >= 1e-33);
+}
+
 // Host: the cap's factors. The degree 7 polynomial is evaluated in s^2 with
 // scaled coefficients; where those would leave FP32's comfortable range
 // (scale / cap beyond 1e-6 .. 1e4) it is not used.

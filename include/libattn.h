@@ -315,8 +315,9 @@ ATTN_API size_t attn_score_workspace_size(int B, int N);
  * exact zero, and zero times infinity is not). KV tiles that no row of a
  * query tile sees are skipped. The cap's tanh is exact to 6e-7 of the score.
  * workspace (attn_score_workspace_size bytes) is needed with row_ranges only.
- * score_cap negative, infinite or NaN, scale not positive and finite, N >
- * 2^24: ATTN_ERR_SHAPE.
+ * score_cap other than 0 outside 1e-12 .. 1e30 (NaN included) or scale /
+ * score_cap outside 1e-33 .. 1e30, scale not positive and finite, N > 2^24:
+ * ATTN_ERR_SHAPE.
  */
 ATTN_API attn_status attn_fwd_score(const void* q, const void* k, const void* v, void* o, float* lse,
                                     const int* row_ranges, const float* slopes, void* workspace, size_t ws_bytes,
@@ -400,8 +401,8 @@ ATTN_API size_t attn_decode_cache_fp8_workspace_size(int B, int Hq, int d, int n
  * blocks may be cut into. The blocks of all sequences are dealt out evenly,
  * whatever their lengths, and a second kernel combines the pieces; with one
  * split a sequence's KV head is one CTA's work. workspace: attn_decode_cache_fp8_workspace_size bytes; concurrent
- * calls need workspaces of their own. score_cap negative, infinite or NaN:
- * ATTN_ERR_SHAPE.
+ * calls need workspaces of their own. score_cap out of attn_fwd_score's
+ * range: ATTN_ERR_SHAPE.
  */
 ATTN_API attn_status attn_decode_cache_fp8(const void* q, const void* k8, const void* v8, const float* sk,
                                            const float* sv, const int* block_table, const int* seqlens,

@@ -186,6 +186,34 @@ def test_scores_at_either_end_of_the_cap(cap, d, dtype, ranges):
     assert (np.abs(lse.double().cpu().numpy() - rl) <= dx + 2.0 ** -20 * (1 + np.abs(rl))).all()
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_the_smallest_and_the_largest_cap(d):
+    """1e-12: uniform weights and no gradient of the scores; 1e30: no cap at all."""
+    q, k, v, do = (x.cuda() for x in inputs.normal(56, [(1, 2, 200, d)] * 4))
+    ws = torch.empty(L.attn_bwd_score_workspace_size(1, 2, 2, 200, d), dtype=U8, device="cuda")
+
+    def step(cap):
+        o, lse, g = torch.empty_like(q), torch.empty((1, 2, 200), device="cuda"), [torch.empty_like(q) for _ in range(3)]
+        L.attn_fwd_score(q, k, v, o, lse, score_cap=cap, window=(-1, 0))
+        L.attn_bwd_score(q, k, v, o, lse, do, *g, ws, score_cap=cap, window=(-1, 0))
+        return [x.double() for x in (o, lse, *g)]
+
+    plain, small, large = step(0.0), step(1e-12), step(1e30)
+    assert L.attn_get_device_status() == 0
+    n = torch.arange(1, 201, device="cuda", dtype=torch.float64)
+    assert (small[1] - n.log()).abs().max() <= 2.0 ** -20 * (1 + math.log(200))
+    mean = v.double().cumsum(2) / n[:, None]
+    size = v.double().abs().cumsum(2) / n[:, None]
+    assert ((small[0] - mean).abs() <= 2.0 ** -8 * 1.05 * (mean.abs() + size)).all()
+    for i in (2, 3):   # 1 - tanh^2 is zero but for the rounding of its square, 2^-22
+        assert small[i].norm() <= 2.0 ** -20 * plain[i].norm()
+    # the same scores by another way: each output within two roundings (2^-8 of its sums; gradients as against float64)
+    assert (large[1] - plain[1]).abs().max() <= 2.0 ** -18
+    assert ((large[0] - plain[0]).abs() <= 2.0 ** -7 * (plain[0].abs() + v.double().abs().max())).all()
+    for a, b in zip(large[2:], plain[2:]):
+        assert (a - b).norm() <= 1e-2 * b.norm()
+
+
 @pytest.mark.parametrize("B,N", [(2, 500), (20, 1000)])
 def test_one_workspace_used_again_at_once(B, N):
     """Calls behind one another with other masks and one workspace: each sees its own tile facts."""

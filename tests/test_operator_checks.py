@@ -91,6 +91,20 @@ def test_score_refusals(lib):
     assert bwd(d=32) == 4 and bwd(Hkv=3) == 5 and bwd(dt=2) == 6 and bwd(wb=wb_ - 1) == 7
 
 
+def test_caps_out_of_range(lib):
+    """Caps whose square, or whose ratio to the scale, leaves float32."""
+    w = L.attn_bwd_score_workspace_size(1, 1, 1, 64, 64)
+
+    def calls(cap, scale=0.1):
+        return (lib.attn_fwd_score(P(), P(), P(), P(), P(), None, None, None, 0, 1, 1, 1, 64, 64, scale, cap, -1, -1, 0, None),
+                lib.attn_bwd_score(P(), P(), P(), P(), P(), P(), P(), P(), P(), None, None, P(), w, 1, 1, 1, 64, 64, scale, cap, -1, -1,
+                                   0, None),
+                lib.attn_decode_cache_fp8(P(), P(), P(), P(), P(), None, P(), None, P(), P(), P(), 256, 1, 1, 1, 128, 0, 64, scale,
+                                          cap, -1, 1, 0, None))
+    for cap, scale in ((1e-13, 0.1), (1e-45, 0.1), (2e30, 0.1), (3e38, 0.1), (-1e-13, 0.1), (1e-12, 1e30), (1e10, 1e-25), (math.nan, 0.1)):
+        assert calls(cap, scale) == (3, 3, 3), (cap, scale)
+
+
 class _Lib:
     def __init__(self):
         self.calls = []
